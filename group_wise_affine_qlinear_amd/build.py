@@ -18,7 +18,7 @@ LIB_NAME = "libqlinear.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["gemm3.hip", "gemm3o.hip", "gemm4.hip", "gemm2.hip", "host.cpp", "gemm.hip", "skinny.hip", "gemv.hip", "misc.hip",
-           "layout.hip"]
+           "layout.hip", "norm.hip", "adapters.hip"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",

@@ -879,3 +879,152 @@ QL_API int qlinear_dequantize(const uint32_t *packed_q, const void *scales, cons
              ? QL_OK
              : QL_EHIP;
 }
+
+namespace {
+
+bool on_elements(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool dtype_ok(int t) { return t == QL_OUT_F32 || t == QL_OUT_BF16; }
+size_t dtype_bytes(int t) { return t == QL_OUT_BF16 ? 2 : 4; }
+
+// A norm's kind and eps: eps of RMS and LAYER between 1e-30 and 1e30 (a row of
+// zeros then stays zero and squares below fp32's range do not matter beside it).
+bool norm_ok(int kind, float eps) {
+  if (kind == QL_NORM_NONE) return true;
+  return (kind == QL_NORM_RMS || kind == QL_NORM_LAYER) && eps >= 1e-30f && eps <= 1e30f;
+}
+
+constexpr int64_t kMaxNormRow = 65536;  // 16 waves of 64 lanes, 64 values each
+constexpr int64_t kMaxAdapterRank = 256;
+constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / 256 - 1;  // a grid holds fewer than 2^32 threads
+constexpr int64_t kMaxNormBlocks = (int64_t(1) << 32) / 1024 - 1;
+
+bool adapter_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t adapters) {
+  return M >= 0 && N >= 0 && K >= 0 && K % kGroup == 0 && adapters >= 0 && M <= INT32_MAX && N <= INT32_MAX &&
+         K <= INT32_MAX && adapters <= INT32_MAX;
+}
+bool adapter_rank_ok(int64_t rank) { return rank >= 8 && rank <= kMaxAdapterRank && rank % 8 == 0; }
+
+size_t adapter_ws(const ql::AdapterPlan &p, int64_t M, int64_t rank, int64_t adapters) {
+  return adapters == 0 ? 0 : (size_t)p.splits * (size_t)M * (size_t)rank * 4u;
+}
+
+}  // namespace
+
+QL_API int qlinear_block_norm(const ql_block_norm_args *a, void *stream) {
+  if (!a) return QL_EINVAL;
+  if (a->M < 0 || a->D < 1) return QL_EINVAL;
+  if (a->D > kMaxNormRow) return QL_EUNSUPPORTED;
+  if (!dtype_ok(a->residual_dtype) || (a->y && !dtype_ok(a->y_dtype))) return QL_EINVAL;
+  const bool before = a->h || a->x16;
+  if (!std::isfinite(a->residual_scale)) return QL_EINVAL;
+  if (!norm_ok(a->post_norm, a->post_eps) || !norm_ok(a->pre_norm, a->pre_eps)) return QL_EINVAL;
+  if (a->M == 0) return QL_OK;
+  if (!a->residual || (!before && !a->residual_out)) return QL_EINVAL;
+  if ((a->x16 != nullptr) != (a->rowscale != nullptr)) return QL_EINVAL;
+  // what belongs to an update without one, or to an h that nothing asks for
+  if (!a->y && (a->residual_out || a->gate || a->post_weight || a->post_bias || a->post_norm != QL_NORM_NONE))
+    return QL_EINVAL;
+  if (!before && (a->pre_norm != QL_NORM_NONE || a->pre_weight || a->pre_bias || a->scale || a->shift))
+    return QL_EINVAL;
+  if ((a->gate && a->gate_ld < a->D) || (a->scale && a->scale_ld < a->D) || (a->shift && a->shift_ld < a->D))
+    return QL_EINVAL;
+  if (a->row_sample ? a->samples < 0 : a->mod_rows < 0) return QL_EINVAL;
+  if (!on_elements(a->residual, dtype_bytes(a->residual_dtype)) ||
+      !on_elements(a->residual_out, dtype_bytes(a->residual_dtype)) || !on_elements(a->y, dtype_bytes(a->y_dtype)) ||
+      !on_elements(a->h, 2) || !on_elements(a->x16, 2))
+    return QL_EALIGN;
+  for (const void *p : {(const void *)a->post_weight, (const void *)a->post_bias, (const void *)a->gate,
+                        (const void *)a->pre_weight, (const void *)a->pre_bias, (const void *)a->scale,
+                        (const void *)a->shift, (const void *)a->row_sample, (const void *)a->rowscale})
+    if (!on_elements(p, 4)) return QL_EALIGN;
+  if (a->M > kMaxNormBlocks) return QL_EUNSUPPORTED;
+  ql::BlockNormArgs k{};
+  k.M = a->M;
+  k.D = (int)a->D;
+  k.residual = a->residual;
+  k.y = a->y;
+  k.residual_out = a->residual_out;
+  k.h = static_cast<uint16_t *>(a->h);
+  k.x16 = static_cast<uint16_t *>(a->x16);
+  k.rowscale = a->rowscale;
+  k.residual_bf16 = a->residual_dtype == QL_OUT_BF16;
+  k.y_bf16 = a->y_dtype == QL_OUT_BF16;
+  k.post_norm = a->post_norm;
+  k.pre_norm = a->pre_norm;
+  k.post_eps = a->post_eps;
+  k.pre_eps = a->pre_eps;
+  k.residual_scale = a->residual_scale;
+  k.post_weight = a->post_weight;
+  k.post_bias = a->post_bias;
+  k.pre_weight = a->pre_weight;
+  k.pre_bias = a->pre_bias;
+  k.gate = a->gate;
+  k.scale = a->scale;
+  k.shift = a->shift;
+  k.gate_ld = a->gate ? a->gate_ld : 0;
+  k.scale_ld = a->scale ? a->scale_ld : 0;
+  k.shift_ld = a->shift ? a->shift_ld : 0;
+  k.row_sample = a->row_sample;
+  k.samples = a->row_sample ? a->samples : 0;
+  k.mod_rows = a->row_sample ? 0 : a->mod_rows;
+  set_last_path(a->y ? (before ? "block_norm_between" : "block_norm_after") : "block_norm_before");
+  return ql::launch_block_norm(k, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? QL_OK : QL_EHIP;
+}
+
+QL_API size_t qlinear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters) {
+  if (!adapter_sizes_ok(M, N, K, adapters) || !adapter_rank_ok(rank) || M == 0 || N == 0) return 0;
+  return adapter_ws(ql::adapter_plan(M, N, K, (int)rank, adapters), M, rank, adapters);
+}
+
+QL_API int qlinear_adapters(const ql_adapter_args *a, void *stream) {
+  if (!a) return QL_EINVAL;
+  if (!adapter_sizes_ok(a->M, a->N, a->K, a->adapters)) return QL_EINVAL;
+  if (!adapter_rank_ok(a->rank)) return QL_EUNSUPPORTED;
+  if (a->ab_dtype != QL_ADAPTER_BF16 && a->ab_dtype != QL_ADAPTER_F16) return QL_EINVAL;
+  if (!dtype_ok(a->out_dtype) || (a->y && !dtype_ok(a->y_dtype))) return QL_EINVAL;
+  if (a->epilogue != QL_EPI_NONE && a->epilogue != QL_EPI_SWIGLU && a->epilogue != QL_EPI_GATE_RESIDUAL) return QL_EINVAL;
+  const bool glu = a->epilogue == QL_EPI_SWIGLU, gated = a->epilogue == QL_EPI_GATE_RESIDUAL;
+  if (glu && a->N % 2) return QL_EINVAL;
+  if (a->M == 0 || a->N == 0) return QL_OK;
+  if (!a->out || !a->row_adapter) return QL_EINVAL;
+  if (a->adapters > 0 && (!a->b || (a->K > 0 && (!a->x || !a->a)))) return QL_EINVAL;
+  if (gated && (!a->residual || !a->gate || a->gate_rows < 1)) return QL_EINVAL;
+  if (a->y == a->out && (glu || a->y_dtype != a->out_dtype)) return QL_EINVAL;
+  if (!aligned16(a->x) || !aligned16(a->a) || !aligned16(a->b) || !aligned16(a->workspace)) return QL_EALIGN;
+  if (!on_elements(a->out, dtype_bytes(a->out_dtype)) || (a->y && !on_elements(a->y, dtype_bytes(a->y_dtype))) ||
+      (gated && (!on_elements(a->residual, dtype_bytes(a->out_dtype)) || !on_elements(a->gate, 4))) ||
+      !on_elements(a->row_adapter, 4) || !on_elements(a->ranks, 4) || !on_elements(a->scaling, 4))
+    return QL_EALIGN;
+  const ql::AdapterPlan p = ql::adapter_plan(a->M, a->N, a->K, (int)a->rank, a->adapters);
+  const int64_t width = glu ? a->N / 2 : a->N;
+  if (p.tiles * ((width + 255) / 256) * p.slots > kMaxBlocks) return QL_EUNSUPPORTED;
+  const size_t need = adapter_ws(p, a->M, a->rank, a->adapters);
+  if (need > 0 && (!a->workspace || a->workspace_bytes < need)) return QL_EWORKSPACE;
+  ql::AdapterArgs k{};
+  k.x = static_cast<const uint16_t *>(a->x);
+  k.a = static_cast<const uint16_t *>(a->a);
+  k.b = static_cast<const uint16_t *>(a->b);
+  k.ab_f16 = a->ab_dtype == QL_ADAPTER_F16;
+  k.M = a->M;
+  k.N = a->N;
+  k.K = a->K;
+  k.adapters = a->adapters;
+  k.rank = (int)a->rank;
+  k.row_adapter = a->row_adapter;
+  k.ranks = a->ranks;
+  k.scaling = a->scaling;
+  k.y = a->y;
+  k.y_bf16 = a->y_dtype == QL_OUT_BF16;
+  k.out = a->out;
+  k.out_bf16 = a->out_dtype == QL_OUT_BF16;
+  k.epilogue = a->epilogue;
+  k.residual = gated ? a->residual : nullptr;
+  k.gate = gated ? a->gate : nullptr;
+  k.gate_rows = gated ? a->gate_rows : 1;
+  k.v = static_cast<float *>(a->workspace);
+  k.vec = width % 4 == 0 && aligned16(a->out) && aligned16(a->y) && aligned16(k.residual) && aligned16(k.gate);
+  char buf[160];
+  std::snprintf(buf, sizeof(buf), "adapters_rows%d_slots%d_split%d", p.row_tile, p.slots, p.splits);
+  set_last_path(buf);
+  return ql::launch_adapters(k, p, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? QL_OK : QL_EHIP;
+}

@@ -141,4 +141,58 @@ hipError_t launch_quantize(int bits, const float *w, int64_t N, int64_t K, uint3
 hipError_t launch_quantize_imatrix(int bits, const float *w, const float *imp, int64_t N, int64_t K,
                                   uint32_t *packed, uint16_t *s, uint16_t *b, int *status, hipStream_t stream);
 
+// Norms around a block (norm.hip); fields as ql_block_norm_args, validated.
+struct BlockNormArgs {
+  int64_t M;
+  int D;
+  const void *residual;   // [M, D]
+  const void *y;          // [M, D], or null: no update
+  void *residual_out;     // or null
+  uint16_t *h;            // bf16, or null
+  uint16_t *x16;          // fp16 with rowscale, or null
+  float *rowscale;
+  int residual_bf16, y_bf16;
+  int post_norm, pre_norm;  // ql_norm
+  float post_eps, pre_eps, residual_scale;
+  const float *post_weight, *post_bias, *pre_weight, *pre_bias;  // [D] or null
+  const float *gate, *scale, *shift;                             // [samples, D] or null
+  int64_t gate_ld, scale_ld, shift_ld;
+  int64_t mod_rows;              // rows per sample; 0: one sample
+  const int32_t *row_sample;     // [M] or null
+  int64_t samples;               // with row_sample
+};
+hipError_t launch_block_norm(const BlockNormArgs &a, hipStream_t stream);
+
+// Low-rank adapters (adapters.hip); fields as ql_adapter_args, validated.
+struct AdapterArgs {
+  const uint16_t *x;        // bf16 [M, K]
+  const uint16_t *a;        // [adapters, rank, K]
+  const uint16_t *b;        // [adapters, N, rank]
+  int ab_f16;
+  int64_t M, N, K, adapters;
+  int rank;
+  const int32_t *row_adapter;  // [M]
+  const int32_t *ranks;        // [adapters] or null
+  const float *scaling;        // [adapters] or null
+  const void *y;               // [M, N] or null
+  int y_bf16;
+  void *out;
+  int out_bf16;
+  int epilogue;                // ql_epilogue
+  const void *residual;
+  const float *gate;
+  int64_t gate_rows;
+  float *v;                    // workspace: [splits, M, rank]
+  int vec;                     // every row of y, out, residual and gate on 4 elements
+};
+// How a call's rows and K are divided over blocks (a function of the sizes only).
+struct AdapterPlan {
+  int row_tile;    // rows per block
+  int slots;       // blocks that share the adapters of one row tile
+  int splits;      // K ranges, fp32 partials in the workspace
+  int64_t tiles;
+};
+AdapterPlan adapter_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t adapters);
+hipError_t launch_adapters(const AdapterArgs &a, const AdapterPlan &p, hipStream_t stream);
+
 }  // namespace ql

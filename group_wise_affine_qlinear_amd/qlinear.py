@@ -23,6 +23,8 @@ QL_PATH_AUTO, QL_PATH_SKINNY, QL_PATH_GEMM, QL_PATH_SPLITK = 0, 1, 2, 3
 QL_LAYOUT_CANONICAL, QL_LAYOUT_TILED = 0, 1
 QL_MODE_AUTO, QL_MODE_EXACT, QL_MODE_FAST, QL_MODE_SPLIT = 0, 1, 2, 3
 QL_EPI_NONE, QL_EPI_SWIGLU, QL_EPI_GATE_RESIDUAL = 0, 1, 2
+QL_NORM_NONE, QL_NORM_RMS, QL_NORM_LAYER = 0, 1, 2
+QL_ADAPTER_BF16, QL_ADAPTER_F16 = 0, 1
 
 EXPORTED = (
     "qlinear_forward", "qlinear_forward_ex", "qlinear_workspace_bytes", "qlinear_packed_words",
@@ -33,6 +35,7 @@ EXPORTED = (
     "qlinear_repack_glu",
     "qlinear_unrepack_glu", "qlinear_quantize_imatrix", "qlinear_forward_workspace_bytes",
     "qlinear_forward_noalloc", "qlinear_forward_noalloc_max_scratch",
+    "qlinear_block_norm", "qlinear_adapters", "qlinear_adapters_workspace_bytes",
 )
 
 
@@ -70,6 +73,66 @@ class ql_forward_args(ctypes.Structure):
         ("residual", ctypes.c_void_p),
         ("gate", ctypes.c_void_p),
         ("gate_rows", ctypes.c_int64),
+    ]
+
+
+class ql_block_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64),
+        ("D", ctypes.c_int64),
+        ("residual", ctypes.c_void_p),
+        ("residual_dtype", ctypes.c_int),
+        ("residual_scale", ctypes.c_float),
+        ("y", ctypes.c_void_p),
+        ("y_dtype", ctypes.c_int),
+        ("post_norm", ctypes.c_int),
+        ("post_eps", ctypes.c_float),
+        ("post_weight", ctypes.c_void_p),
+        ("post_bias", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("gate_ld", ctypes.c_int64),
+        ("residual_out", ctypes.c_void_p),
+        ("pre_norm", ctypes.c_int),
+        ("pre_eps", ctypes.c_float),
+        ("pre_weight", ctypes.c_void_p),
+        ("pre_bias", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("scale_ld", ctypes.c_int64),
+        ("shift", ctypes.c_void_p),
+        ("shift_ld", ctypes.c_int64),
+        ("mod_rows", ctypes.c_int64),
+        ("row_sample", ctypes.c_void_p),
+        ("samples", ctypes.c_int64),
+        ("h", ctypes.c_void_p),
+        ("x16", ctypes.c_void_p),
+        ("rowscale", ctypes.c_void_p),
+    ]
+
+
+class ql_adapter_args(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("a", ctypes.c_void_p),
+        ("b", ctypes.c_void_p),
+        ("ab_dtype", ctypes.c_int),
+        ("M", ctypes.c_int64),
+        ("N", ctypes.c_int64),
+        ("K", ctypes.c_int64),
+        ("adapters", ctypes.c_int64),
+        ("rank", ctypes.c_int64),
+        ("row_adapter", ctypes.c_void_p),
+        ("ranks", ctypes.c_void_p),
+        ("scaling", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("y_dtype", ctypes.c_int),
+        ("out", ctypes.c_void_p),
+        ("out_dtype", ctypes.c_int),
+        ("epilogue", ctypes.c_int),
+        ("residual", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("gate_rows", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -121,6 +184,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "qlinear_unrepack": ([vp, vp, i32, i32, i64, i64, vp, vp, vp, vp], i32),
         "qlinear_repack_glu": ([vp, vp, vp, i32, i32, i64, i64, vp, vp, vp], i32),
         "qlinear_unrepack_glu": ([vp, vp, i32, i32, i64, i64, vp, vp, vp, vp], i32),
+        "qlinear_block_norm": ([ctypes.POINTER(ql_block_norm_args), vp], i32),
+        "qlinear_adapters": ([ctypes.POINTER(ql_adapter_args), vp], i32),
+        "qlinear_adapters_workspace_bytes": ([i64, i64, i64, i64, i64], sz),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -455,6 +521,192 @@ def qlinear_dequantize(packed_q, scales, biases, bits, group, N, K, w_out, strea
         _stream_handle(stream))
     _check(st, "qlinear_dequantize")
     return w_out
+
+
+# ------------------------------------------------------------------ around a projection
+
+def _operand(t, name, dtypes, shape, device):
+    """Data pointer of a contiguous tensor of one of the dtypes, of this shape, on this device."""
+    if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    _dev_ptr(t, name, dtypes, shape)
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _value_dtype(t, name):
+    """ql_out_dtype of a stream of values."""
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return QL_OUT_F32
+    if t.dtype == torch.bfloat16:
+        return QL_OUT_BF16
+    raise TypeError(f"{name} must be float32 or bfloat16")
+
+
+def _modulation(t, name, rows, D, device):
+    """(pointer, row pitch) of a [samples, D] fp32 tensor whose rows may be slices of longer ones."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+        raise TypeError(f"{name} must be a float32 tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 2 or t.shape[1] != D or t.shape[0] < rows:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [>= {rows}, {D}]")
+    if (D > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < D):
+        raise ValueError(f"{name} must have rows of consecutive values that do not overlap")
+    return t.data_ptr(), max(t.stride(0), D)
+
+
+def _launch(fn, where, args, device, stream):
+    """Calls a C entry point on `stream` (default: the current stream of the tensors' device) with that device current."""
+    torch = _torch()
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif not isinstance(stream, int) and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, expected {device}")
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if device.index == torch.cuda.current_device():
+        st = fn(ctypes.byref(args), handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(ctypes.byref(args), handle)
+    if st != QL_OK:
+        raise QLinearError(st, where)
+
+
+def qlinear_block_norm(residual, M, D, *, y=None, residual_scale=1.0, post_norm=QL_NORM_NONE, post_eps=1e-6,
+                       post_weight=None, post_bias=None, gate=None, residual_out=None, pre_norm=QL_NORM_NONE,
+                       pre_eps=1e-6, pre_weight=None, pre_bias=None, scale=None, shift=None, mod_rows=0,
+                       row_sample=None, samples=None, h=None, x16=None, rowscale=None, stream=None):
+    """C ``qlinear_block_norm``: the norms before and after a block with modulation, gate and residual.
+
+    ``z = N_post(y) * post_weight + post_bias``; ``r = residual_scale * residual + gate[s] * z`` goes to
+    ``residual_out`` (may be ``residual``); ``h = (N_pre(r) * pre_weight + pre_bias) * (1 + scale[s]) + shift[s]``
+    goes to ``h`` (bf16) and/or ``x16``/``rowscale`` (FAST activations). ``residual``, ``residual_out`` and ``y``
+    are fp32 or bf16 [M, D]; ``gate``, ``scale`` and ``shift`` fp32 [samples, D], slices of a wider modulation
+    output included. The sample of row m is ``m // mod_rows`` (``mod_rows`` 0: one sample) or ``row_sample[m]``
+    (int32); a row whose sample is outside [0, samples) is left as it is. ``samples`` defaults to the rows of
+    the modulation arrays given with ``row_sample``.
+    """
+    torch = _torch()
+    lib = load_library()
+    if not isinstance(residual, torch.Tensor):
+        raise TypeError("residual must be a torch tensor")
+    dev = residual.device
+    shape = (M, D)
+    f32, stream_types = (torch.float32,), (torch.float32, torch.bfloat16)
+    a = ql_block_norm_args()
+    a.M, a.D, a.residual_scale = M, D, residual_scale
+    a.residual = _operand(residual, "residual", stream_types, shape, dev)
+    a.residual_dtype = _value_dtype(residual, "residual")
+    if dev.type != "cuda":
+        raise ValueError("residual must be a device tensor")
+    if y is not None:
+        a.y = _operand(y, "y", stream_types, shape, dev)
+        a.y_dtype = _value_dtype(y, "y")
+    a.post_norm, a.post_eps, a.pre_norm, a.pre_eps = post_norm, post_eps, pre_norm, pre_eps
+    if post_weight is not None:
+        a.post_weight = _operand(post_weight, "post_weight", f32, (D,), dev)
+    if post_bias is not None:
+        a.post_bias = _operand(post_bias, "post_bias", f32, (D,), dev)
+    if pre_weight is not None:
+        a.pre_weight = _operand(pre_weight, "pre_weight", f32, (D,), dev)
+    if pre_bias is not None:
+        a.pre_bias = _operand(pre_bias, "pre_bias", f32, (D,), dev)
+    if row_sample is not None:
+        a.row_sample = _operand(row_sample, "row_sample", (torch.int32,), (M,), dev)
+        if samples is None:
+            given = [t.shape[0] for t in (gate, scale, shift) if t is not None]
+            if not given:
+                raise ValueError("row_sample without gate, scale or shift needs samples")
+            samples = min(given)
+        a.samples = need = samples
+    else:
+        a.mod_rows = mod_rows
+        need = -(-M // mod_rows) if mod_rows > 0 else 1
+    if gate is not None:
+        a.gate, a.gate_ld = _modulation(gate, "gate", need, D, dev)
+    if scale is not None:
+        a.scale, a.scale_ld = _modulation(scale, "scale", need, D, dev)
+    if shift is not None:
+        a.shift, a.shift_ld = _modulation(shift, "shift", need, D, dev)
+    if residual_out is not None:
+        a.residual_out = _operand(residual_out, "residual_out", (residual.dtype,), shape, dev)
+    if h is not None:
+        a.h = _operand(h, "h", (torch.bfloat16,), shape, dev)
+    if x16 is not None:
+        a.x16 = _operand(x16, "x16", (torch.float16,), shape, dev)
+    if rowscale is not None:
+        a.rowscale = _operand(rowscale, "rowscale", f32, (M,), dev)
+    _launch(lib.qlinear_block_norm, "qlinear_block_norm", a, dev, stream)
+
+
+def qlinear_adapters_workspace_bytes(M, N, K, rank, adapters) -> int:
+    return int(load_library().qlinear_adapters_workspace_bytes(M, N, K, rank, adapters))
+
+
+def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, scaling=None, epilogue=QL_EPI_NONE,
+                     residual=None, gate=None, gate_rows=0, workspace=TORCH_WORKSPACE, stream=None):
+    """C ``qlinear_adapters``: low-rank adapters of many requests beside a projection they share.
+
+    ``t[m] = y[m] + scaling[id] * b[id] @ (a[id] @ x[m])`` with ``id = row_adapter[m]`` (int32; outside the
+    table: no adapter), then ``out = t`` or an epilogue of it. ``x`` bf16 [M, K]; ``a`` [adapters, rank, K] and
+    ``b`` [adapters, N, rank], both bf16 or both fp16; ``ranks`` int32 and ``scaling`` fp32 [adapters]; ``y``
+    [M, N] and ``out`` fp32 or bf16 (``out`` may be ``y``). ``epilogue=QL_EPI_SWIGLU`` writes ``out`` [M, N/2]
+    = silu(t[:, :N/2]) * t[:, N/2:]; ``epilogue=QL_EPI_GATE_RESIDUAL`` writes ``residual`` +
+    ``gate``[m // ``gate_rows``] * t. ``workspace`` is a device tensor of
+    ``qlinear_adapters_workspace_bytes`` bytes, by default one from torch's caching allocator.
+    """
+    torch = _torch()
+    lib = load_library()
+    if not isinstance(a, torch.Tensor) or a.dim() != 3:
+        raise ValueError("a must be a tensor [adapters, rank, K]")
+    dev = out.device
+    if dev.type != "cuda":
+        raise ValueError("out must be a device tensor")
+    n, rank = a.shape[0], a.shape[1]
+    f = ql_adapter_args()
+    f.M, f.N, f.K, f.adapters, f.rank = M, N, K, n, rank
+    if a.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("a must be bfloat16 or float16")
+    f.ab_dtype = QL_ADAPTER_F16 if a.dtype == torch.float16 else QL_ADAPTER_BF16
+    f.x = _operand(x, "x", (torch.bfloat16, torch.int16, torch.uint16), (M, K), dev)
+    f.a = _operand(a, "a", (a.dtype,), (n, rank, K), dev)
+    f.b = _operand(b, "b", (a.dtype,), (n, N, rank), dev)
+    f.row_adapter = _operand(row_adapter, "row_adapter", (torch.int32,), (M,), dev)
+    if ranks is not None:
+        f.ranks = _operand(ranks, "ranks", (torch.int32,), (n,), dev)
+    if scaling is not None:
+        f.scaling = _operand(scaling, "scaling", (torch.float32,), (n,), dev)
+    if y is not None:
+        f.y = _operand(y, "y", (torch.float32, torch.bfloat16), (M, N), dev)
+        f.y_dtype = _value_dtype(y, "y")
+    f.out_dtype = _value_dtype(out, "out")
+    f.out = _operand(out, "out", (out.dtype,), (M, N // 2 if epilogue == QL_EPI_SWIGLU else N), dev)
+    f.epilogue = epilogue
+    if epilogue == QL_EPI_GATE_RESIDUAL:
+        f.gate_rows = gate_rows
+        if residual is not None:
+            f.residual = _operand(residual, "residual", (out.dtype,), (M, N), dev)
+        if gate is not None and gate_rows >= 1:
+            f.gate = _operand(gate, "gate", (torch.float32,), (-(-M // gate_rows), N), dev)
+    if isinstance(workspace, str):
+        if workspace != TORCH_WORKSPACE:
+            raise ValueError(f"workspace must be a device tensor, None or {TORCH_WORKSPACE!r}")
+        nbytes = lib.qlinear_adapters_workspace_bytes(M, N, K, rank, n)
+        workspace = None
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            if stream is not None:
+                # taken on the current stream: kept from reuse until the call's stream is done with it
+                workspace.record_stream(torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream)
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        f.workspace = workspace.data_ptr()
+        f.workspace_bytes = workspace.numel() * workspace.element_size()
+    _launch(lib.qlinear_adapters, "qlinear_adapters", f, dev, stream)
+    return out
 
 
 # ------------------------------------------------------------------ host entry points

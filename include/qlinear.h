@@ -420,6 +420,136 @@ int qlinear_unrepack(const uint32_t *tiled_q, const uint32_t *tiled_sb, int bits
                      int64_t N, int64_t K, uint32_t *packed_q, void *scales, void *biases,
                      void *stream);
 
+/* Norms of qlinear_block_norm over the D values v of a row:
+ * NONE v; RMS v / sqrt(mean(v^2) + eps); LAYER (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps). */
+typedef enum { QL_NORM_NONE = 0, QL_NORM_RMS = 1, QL_NORM_LAYER = 2 } ql_norm;
+
+/* Arguments of qlinear_block_norm. Zero-initialise, then fill (residual_scale
+ * is usually 1; NULL pointers leave their factor or term out). */
+typedef struct ql_block_norm_args {
+  int64_t M, D;                /* rows; row length, 1 .. 65536                  */
+  const void *residual;        /* [M, D] residual stream                        */
+  int residual_dtype;          /* ql_out_dtype of residual and residual_out     */
+  float residual_scale;        /* finite                                        */
+  const void *y;               /* [M, D] output of the block, or NULL           */
+  int y_dtype;                 /* ql_out_dtype                                  */
+  int post_norm;               /* ql_norm of y                                  */
+  float post_eps;              /* with RMS and LAYER: 1e-30 .. 1e30             */
+  const float *post_weight;    /* fp32 [D] or NULL                              */
+  const float *post_bias;      /* fp32 [D] or NULL                              */
+  const float *gate;           /* fp32, row of sample s at gate + s * gate_ld, or NULL */
+  int64_t gate_ld;             /* >= D                                          */
+  void *residual_out;          /* [M, D], may be residual; needs y              */
+  int pre_norm;                /* ql_norm of the updated stream                 */
+  float pre_eps;
+  const float *pre_weight;     /* fp32 [D] or NULL                              */
+  const float *pre_bias;       /* fp32 [D] or NULL                              */
+  const float *scale;          /* fp32, sample s at scale + s * scale_ld, or NULL */
+  int64_t scale_ld;            /* >= D                                          */
+  const float *shift;          /* fp32, sample s at shift + s * shift_ld, or NULL */
+  int64_t shift_ld;            /* >= D                                          */
+  int64_t mod_rows;            /* rows per sample: s = m / mod_rows; 0: one sample */
+  const int32_t *row_sample;   /* int32 [M]: s per row instead (mod_rows ignored), or NULL */
+  int64_t samples;             /* with row_sample: samples that gate, scale and shift hold */
+  void *h;                     /* bf16 [M, D] or NULL                           */
+  void *x16;                   /* fp16 [M, D] with                              */
+  float *rowscale;             /* [M], or both NULL                             */
+} ql_block_norm_args;
+
+/*
+ * The norms before and after a block of the DiT with the AdaLN modulation,
+ * the tanh gate and the scaled residual update, in one pass over the rows:
+ *
+ *   z = N_post(y) * post_weight + post_bias
+ *   r = residual_scale * residual + gate[s] * z
+ *   h = (N_pre(r) * pre_weight + pre_bias) * (1 + scale[s]) + shift[s]
+ *
+ * with s the sample of the row. Three uses: before a block (y NULL: h from
+ * the residual stream), after it (residual_out), and both between two blocks.
+ * residual_out gets r, h gets h (bf16, the x of a projection), and x16 with
+ * rowscale get h as the FAST activations of qlinear_fast_activations made
+ * from the unrounded h, for ql_forward_args. At least one output is given.
+ * All arithmetic is fp32 (rows whose squares leave fp32 are summed scaled by
+ * a power of two), h is made from the unrounded r, and each output is rounded
+ * once. An infinity or NaN in a row stays in that row's outputs.
+ * With row_sample, a row whose sample is outside [0, samples) is left as it
+ * is: nothing is read for it or written to it (padding behind the last
+ * sequence of a packed batch). gate, scale and shift may be slices of one
+ * modulation output (row pitches gate_ld, scale_ld, shift_ld). residual_out
+ * may be residual; no other output may overlap an input or another output.
+ * Rows that start on 16 bytes in every array (D a multiple of 8, 16-byte
+ * aligned pointers, pitches multiples of 4) are read and written 16 bytes at a
+ * time; any other length or alignment to the element is served, slower.
+ * Returns QL_EINVAL for bad sizes, pitches, norms, eps or missing arrays,
+ * QL_EALIGN for a pointer not aligned to its element, QL_EUNSUPPORTED for
+ * D > 65536. M == 0 is a no-op. No scratch, no allocation, no synchronization.
+ */
+int qlinear_block_norm(const ql_block_norm_args *args, void *stream);
+
+/* Element types of adapter tables. */
+typedef enum { QL_ADAPTER_BF16 = 0, QL_ADAPTER_F16 = 1 } ql_adapter_dtype;
+
+/* Arguments of qlinear_adapters. Zero-initialise, then fill. */
+typedef struct ql_adapter_args {
+  const void *x;               /* bf16 [M, K], the projection's input           */
+  const void *a;               /* [adapters, rank, K]                           */
+  const void *b;               /* [adapters, N, rank]                           */
+  int ab_dtype;                /* ql_adapter_dtype of a and b                   */
+  int64_t M, N, K;             /* N as the projection's (2F with QL_EPI_SWIGLU); K a multiple of 64 */
+  int64_t adapters;            /* adapters in the tables, 0 .. 2^31 - 1         */
+  int64_t rank;                /* rows of a, a multiple of 8, 8 .. 256          */
+  const int32_t *row_adapter;  /* int32 [M]: adapter of each row; outside
+                                  [0, adapters): the row has none               */
+  const int32_t *ranks;        /* int32 [adapters]: rank in use of each adapter
+                                  (clamped to 0 .. rank), or NULL: rank         */
+  const float *scaling;        /* fp32 [adapters], or NULL: 1                   */
+  const void *y;               /* [M, N] output of the shared projection, or NULL: 0 */
+  int y_dtype;                 /* ql_out_dtype                                  */
+  void *out;                   /* [M, N] ([M, N/2] with QL_EPI_SWIGLU)          */
+  int out_dtype;               /* ql_out_dtype                                  */
+  int epilogue;                /* ql_epilogue                                   */
+  const void *residual;        /* QL_EPI_GATE_RESIDUAL: [M, N], dtype of out    */
+  const float *gate;           /* QL_EPI_GATE_RESIDUAL: fp32 [ceil(M/gate_rows), N] */
+  int64_t gate_rows;           /* QL_EPI_GATE_RESIDUAL: rows per gate row, >= 1 */
+  void *workspace;             /* device scratch owned by the caller            */
+  size_t workspace_bytes;      /* >= qlinear_adapters_workspace_bytes           */
+} ql_adapter_args;
+
+/*
+ * Low-rank adapters of many requests beside a projection they share: with id
+ * the adapter of row m,
+ *
+ *   t[m, :] = y[m, :] + scaling[id] * B[id] (A[id] x[m, :])
+ *
+ * (t = y for a row without an adapter), and out = t, or an epilogue of t:
+ * SWIGLU out[m, f] = silu(t[m, f]) * t[m, F + f], f < F = N / 2 (rows of b and
+ * columns of y in the order [gate (F); up (F)]); GATE_RESIDUAL out = residual
+ * + gate[m / gate_rows] * t. y is what qlinear_forward_ex wrote for the same
+ * x (fp32 keeps its sums unrounded until the adapter is added). out may be y
+ * (same dtype, no epilogue or GATE_RESIDUAL) or residual; without an epilogue
+ * a row without an adapter is then left untouched.
+ * Requests of one adapter need not be adjacent, but rows in the order of
+ * their requests run fastest: a tile of consecutive rows is multiplied by
+ * each distinct adapter that occurs in it. What other rows, other adapters or
+ * table entries past an adapter's own rank hold, infinities and NaN included,
+ * never reaches a row. row_adapter, ranks and scaling are read on the device,
+ * so a captured graph serves other requests after they are overwritten.
+ * Sums are fp32: x and the tables enter as they are, A x is kept in fp32 (to
+ * 24 bits in the second product), out is rounded once. A row's result does
+ * not depend on its position or its neighbours in the batch of the same M.
+ * Returns QL_EINVAL for bad sizes, types or missing arrays, QL_EALIGN if x, a,
+ * b or the workspace is not 16-byte aligned or another pointer is not aligned
+ * to its element, QL_EUNSUPPORTED for a rank that is not a multiple of 8 up to
+ * 256, QL_EWORKSPACE for a missing or too small workspace. M == 0 or N == 0 is
+ * a no-op. Calls that share one workspace must not overlap in time; nothing
+ * in it is kept from one call to the next. No allocation, no synchronization.
+ */
+int qlinear_adapters(const ql_adapter_args *args, void *stream);
+
+/* Bytes of workspace a qlinear_adapters call of these sizes needs (fp32
+ * partial sums of A x); 0 for invalid arguments. */
+size_t qlinear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters);
+
 /* Static description of a status code. */
 const char *qlinear_status_string(int status);
 

@@ -82,6 +82,7 @@ __all__ = [
     "fast_weights_f16", "fast_activations_f16", "forward_fast", "forward_fast_rows", "silu", "swiglu",
     "gate_residual", "adaln_modulate", "forward_modulated",
     "IMATRIX_DELTAS", "quantize_imatrix", "weighted_error",
+    "norm_rows", "block_norm", "adapter_delta",
 ]
 
 GROUP = 64
@@ -536,3 +537,46 @@ def timed_forward(x_bf16, packed, s16, b16, bits, k, group: int = GROUP):
     y = gemm_f64(x_bf16, w_hat)
     t2 = time.perf_counter()
     return y, {"dequant_s": t1 - t0, "gemm_s": t2 - t1, "total_s": t2 - t0}
+
+
+# ----------------------------------------------------------------- around a projection
+
+def norm_rows(v: np.ndarray, kind: str, eps: float) -> np.ndarray:
+    """Row norm in fp64: "none" v, "rms" v / sqrt(mean v^2 + eps), "layer" of v - mean v."""
+    v = np.asarray(v, dtype=np.float64)
+    if kind == "none":
+        return v
+    if kind == "layer":
+        v = v - v.mean(axis=1, keepdims=True)
+    elif kind != "rms":
+        raise ValueError(kind)
+    return v / np.sqrt((v * v).mean(axis=1, keepdims=True) + np.float64(np.float32(eps)))
+
+
+def block_norm(residual, y=None, *, residual_scale=1.0, post="none", post_eps=1e-6, post_weight=None, post_bias=None,
+               gate=None, pre="none", pre_eps=1e-6, pre_weight=None, pre_bias=None, scale=None, shift=None):
+    """(r, h) in fp64: r = residual_scale * residual + gate * (N_post(y) * post_weight + post_bias),
+    h = (N_pre(r) * pre_weight + pre_bias) * (1 + scale) + shift. gate, scale and shift are per row [M, D]."""
+    def f64(t, default):
+        return default if t is None else np.asarray(t, dtype=np.float64)
+
+    r = f64(residual, None) * np.float64(np.float32(residual_scale))
+    if y is not None:
+        z = norm_rows(y, post, post_eps) * f64(post_weight, 1.0) + f64(post_bias, 0.0)
+        r = r + f64(gate, 1.0) * z
+    h = norm_rows(r, pre, pre_eps) * f64(pre_weight, 1.0) + f64(pre_bias, 0.0)
+    return r, h * (1.0 + f64(scale, 0.0)) + f64(shift, 0.0)
+
+
+def adapter_delta(x, a, b, row_adapter, ranks=None, scaling=None) -> np.ndarray:
+    """delta[m] = scaling[id] * b[id] (a[id] x[m]) in fp64, id = row_adapter[m]; zero where id is outside the
+    table. ranks: rows of a (columns of b) in use, clamped to the table's rank."""
+    x, a, b = (np.asarray(t, dtype=np.float64) for t in (x, a, b))
+    out = np.zeros((x.shape[0], b.shape[1]))
+    for m, i in enumerate(np.asarray(row_adapter)):
+        if not 0 <= i < a.shape[0]:
+            continue
+        r = a.shape[1] if ranks is None else min(max(int(ranks[i]), 0), a.shape[1])
+        v = a[i, :r] @ x[m]
+        out[m] = (1.0 if scaling is None else float(scaling[i])) * (b[i, :, :r] @ v)
+    return out
