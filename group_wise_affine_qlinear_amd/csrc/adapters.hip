@@ -29,6 +29,8 @@ namespace ql {
 namespace {
 
 constexpr int kWaves = 4;
+constexpr int kMostSplits = 8;
+constexpr int kCus = 256;  // MI355X
 
 // A fragment of eight table values as bf16 terms whose sum is exact.
 template <bool F16> struct Terms { static constexpr int n = F16 ? 2 : 1; };
@@ -108,81 +110,115 @@ __device__ __forceinline__ int adapter_rank(const AdapterArgs &a, int id) {
   return min(max(a.ranks[id], 0), a.rank);
 }
 
-// v = A x over a range of K. Block: MI*16 rows, RJ*16 ranks, four waves that
-// take the range's 64-wide K units in turn and add their sums in LDS in wave
-// order. A lane's 32 bytes of a row (two MFMA steps) lie side by side, so the
-// four lanes of a row read its whole 128-byte line.
-template <int MI, int RJ, bool F16>
+// v = A x over a range of K. Block: WR*MI*16 rows, RJ*16 ranks; its waves are
+// WR along the rows, and the others take the range's 64-wide K units in turn
+// and add their sums in LDS in wave order. A lane's 32 bytes of a row (two
+// MFMA steps) lie side by side, so the four lanes of a row read its whole
+// 128-byte line. With DOUBLE a wave requests its next unit before it
+// multiplies the one it has: at 64-row tiles that is worth more than the waves
+// its registers cost (SwiGLU case of 4096 rows 97 -> 90 us in all); at 16-row
+// tiles, where a wave has one to three units, it is not (10.7 -> 10.8 us).
+template <int MI, int WR, int RJ, bool F16, bool DOUBLE>
 __global__ __launch_bounds__(64 * kWaves) void adapter_down_kernel(AdapterArgs a, int slots, int units_per_split) {
   constexpr int NT = Terms<F16>::n;
-  __shared__ f32x4 red[kWaves - 1][MI * RJ][64];
+  constexpr int T = 16 * MI * WR, KW = kWaves / WR;
+  __shared__ f32x4 red[KW - 1][WR][MI * RJ][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave % WR, wk = wave / WR;
   const int r16 = lane & 15, g = lane >> 4;
-  const int64_t m0 = (int64_t)blockIdx.x * (16 * MI);
+  const int64_t m0 = (int64_t)blockIdx.x * T;
   const int slot = blockIdx.z % slots;
   const int r0 = (int)(blockIdx.z / slots) * (16 * RJ);
   const int units = (int)(a.K / 64);
   const int u0 = blockIdx.y * units_per_split, u1 = min(units, u0 + units_per_split);
-  const int id = tile_id<16 * MI>(a.row_adapter, m0, a.M, a.adapters, lane);
+  const int id = tile_id<T>(a.row_adapter, m0, a.M, a.adapters, lane);
   each_adapter(id, 0, slot, slots, [&](int cur, uint64_t rows) {
     const int rank = adapter_rank(a, cur);
     if (r0 >= rank) return;
-    const uint16_t *xp[MI], *ap[RJ];
+    // rows of x and of the table as offsets into the tile's and the adapter's part
+    const __amdgpu_buffer_rsrc_t x_buf = make_rsrc(a.x, m0 * a.K * 2, INT32_MAX);
+    const __amdgpu_buffer_rsrc_t a_buf = make_rsrc(a.a, ((int64_t)cur * a.rank + r0) * a.K * 2, INT32_MAX);
+    const int first = wr * (16 * MI);
+    int x_at[MI], a_at[RJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int row = i * 16 + r16;
+      const int row = first + i * 16 + r16;
       const int pick = (rows >> row) & 1 ? row : (int)__builtin_ctzll(rows);  // rows of others: not loaded
-      xp[i] = a.x + (m0 + pick) * a.K + g * 16;
+      x_at[i] = pick * (int)a.K * 2 + g * 32;
     }
 #pragma unroll
-    for (int j = 0; j < RJ; ++j)
-      ap[j] = a.a + ((int64_t)cur * a.rank + min(r0 + j * 16 + r16, rank - 1)) * a.K + g * 16;
+    for (int j = 0; j < RJ; ++j) a_at[j] = min(j * 16 + r16, rank - r0 - 1) * (int)a.K * 2 + g * 32;
     f32x4 acc[MI][RJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < RJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int u = u0 + wave; u < u1; u += kWaves) {
-      u32x4 xr[MI][2], ar[RJ][2];
+    struct Unit {
+      u32x4 x[MI][2], a[RJ][2];
+    } one, two;
+    auto load = [&](int u, Unit &t) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) xr[i][s] = *reinterpret_cast<const u32x4 *>(xp[i] + u * 64 + s * 8);
+        for (int s = 0; s < 2; ++s)
+          t.x[i][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x_buf, x_at[i] + s * 16, u * 128, 0));
 #pragma unroll
       for (int j = 0; j < RJ; ++j)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) ar[j][s] = *reinterpret_cast<const u32x4 *>(ap[j] + u * 64 + s * 8);
+        for (int s = 0; s < 2; ++s)
+          t.a[j][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(a_buf, a_at[j] + s * 16, u * 128, 0));
+      if constexpr (DOUBLE) __builtin_amdgcn_sched_barrier(0);  // requested before the other unit is worked on
+    };
+    auto multiply = [&](const Unit &t) {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int j = 0; j < RJ; ++j) {
-          bf16x8 t[NT];
-          table_terms<F16>(ar[j][s], t);
+          bf16x8 w[NT];
+          table_terms<F16>(t.a[j][s], w);
 #pragma unroll
           for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int k = 0; k < NT; ++k) acc[i][j] = mfma(t[k], as_bf16x8(xr[i][s]), acc[i][j]);
+            for (int k = 0; k < NT; ++k) acc[i][j] = mfma(w[k], as_bf16x8(t.x[i][s]), acc[i][j]);
         }
+      if constexpr (DOUBLE) __builtin_amdgcn_sched_barrier(0);
+    };
+    const int last = u1 - 1;
+    if (((rows >> first) & (~0ull >> (64 - 16 * MI))) != 0 && u0 + wk < u1) {
+      if constexpr (DOUBLE) {
+        load(u0 + wk, one);
+        for (int u = u0 + wk; u < u1; u += 2 * KW) {
+          load(min(u + KW, last), two);
+          multiply(one);
+          load(min(u + 2 * KW, last), one);
+          if (u + KW < u1) multiply(two);
+        }
+      } else {
+        for (int u = u0 + wk; u < u1; u += KW) {
+          load(u, one);
+          multiply(one);
+        }
+      }
     }
     __syncthreads();  // the previous adapter's sums have been read
-    if (wave > 0) {
+    if (wk > 0) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < RJ; ++j) red[wave - 1][i * RJ + j][lane] = acc[i][j];
+        for (int j = 0; j < RJ; ++j) red[wk - 1][wr][i * RJ + j][lane] = acc[i][j];
     }
     __syncthreads();
-    if (wave > 0) return;
+    if (wk > 0) return;
     float *v = a.v + (int64_t)blockIdx.y * a.M * a.rank;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int row = i * 16 + r16;
+      const int row = first + i * 16 + r16;
 #pragma unroll
       for (int j = 0; j < RJ; ++j) {
         f32x4 t = acc[i][j];
 #pragma unroll
-        for (int w = 0; w < kWaves - 1; ++w) t += red[w][i * RJ + j][lane];
+        for (int w = 0; w < KW - 1; ++w) t += red[w][wr][i * RJ + j][lane];
         const int r = r0 + j * 16 + g * 4;
         if (((rows >> row) & 1) && r < a.rank) *reinterpret_cast<f32x4 *>(v + (m0 + row) * a.rank + r) = t;
       }
@@ -196,163 +232,325 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
-// out = epilogue(y + scaling * B v). Block: MI*16 rows, 256 output columns, 64
-// per wave: subtile s of a wave covers columns 4*c + s, so that a lane ends
-// with four consecutive columns of four rows and 16 lanes store a contiguous
-// 256 (fp32) or 128 bytes of a row. SwiGLU has the same columns twice, from
-// the gate and the up half.
-template <int MI, bool F16, typename YT, typename OT, int EPI, bool VEC>
+// Sixteen rows from row m of an array [., row_length], as a buffer: at most
+// 16 * 2^22 values (kMaxAdapterColumns) of 4 bytes; of no bytes for no array.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_buffer(const void *p, int64_t m, int64_t row_length, int size) {
+  return make_rsrc(p, p ? m * row_length * size : 0, p ? 16 * row_length * size : 0);
+}
+
+// Four values of a stream as loaded: packed where they come as 8 or 16 bytes.
+template <typename T, bool VEC> struct Raw4 { uint32_t v[VEC && __is_same(T, BF16) ? 2 : 4]; };
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void unpack4(const Raw4<T, VEC> &r, float (&f)[4]) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    if constexpr (VEC && __is_same(T, BF16)) f[s] = s % 2 ? bf16_hi(r.v[s / 2]) : bf16_lo(r.v[s / 2]);
+    else f[s] = __uint_as_float(r.v[s]);
+  }
+}
+
+// Columns n .. n + 3 of rows of `width` values, `pitch` apart. A column past
+// the width, or a row that is not live, has its offset past the buffer's end:
+// its loads give zero and its stores are dropped.
+template <bool VEC> struct Tile {
+  int n, width, pitch;
+  static constexpr int kPast = 0x7FFFFFF0;
+  __device__ __forceinline__ int at(int row, int first, int s, bool live, int size) const {
+    return live && n + s < width ? (row * pitch + first + n + s) * size : kPast;
+  }
+  template <typename T>
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int row, int first, bool live, Raw4<T, VEC> &raw) const {
+    if constexpr (VEC && __is_same(T, F32)) {
+      const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at(row, first, 0, live, 4), 0, 0));
+#pragma unroll
+      for (int s = 0; s < 4; ++s) raw.v[s] = v[s];
+    } else if constexpr (VEC) {
+      const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, at(row, first, 0, live, 2), 0, 0));
+      raw.v[0] = v[0], raw.v[1] = v[1];
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if constexpr (__is_same(T, F32)) raw.v[s] = __builtin_amdgcn_raw_buffer_load_b32(r, at(row, first, s, live, 4), 0, 0);
+        else raw.v[s] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, at(row, first, s, live, 2), 0, 0) << 16;
+      }
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, int row, bool live, const float (&f)[4]) const {
+    if constexpr (VEC && __is_same(T, F32)) {
+      const f32x4 v = {f[0], f[1], f[2], f[3]};
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, at(row, 0, 0, live, 4), 0, 0);
+    } else if constexpr (VEC) {
+      __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])}, r,
+                                            at(row, 0, 0, live, 2), 0, 0);
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if constexpr (__is_same(T, F32))
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[s]), r, at(row, 0, s, live, 4), 0, 0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(f[s]), r, at(row, 0, s, live, 2), 0, 0);
+      }
+    }
+  }
+};
+
+// out = epilogue(y + scaling * B v). Block: MI*16 rows; its four waves take
+// `chunks` times 256 output columns, 64 each. For one adapter of the tile the
+// block first adds the partial sums of v, scales them and keeps them in LDS
+// (fp32, zero past the adapter's rank), so that they are read once per block
+// and not once per 64 columns. Subtile s of a wave covers columns 4*c + s: a
+// lane ends with four consecutive columns of four rows, and 16 lanes load and
+// store a contiguous 256 (fp32) or 128 bytes of a row. SwiGLU has the same
+// columns twice, from the gate and the up half. KB steps of 32 ranks of B
+// stay in registers over the rows (0: any rank, B read again for every 16 rows).
+//
+// One step is 16 rows by 64 columns. What the next step reads of y, residual,
+// gate and B is requested before this step's stores: a wait for loads counts
+// every memory access before them, so a load behind stores waits for those
+// (16384 x 4608 bf16 with residual: 200 us with the loads behind).
+template <int MI, int KB, bool F16, typename YT, typename OT, int EPI, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, int slots, int splits, int col_blocks,
-                                                               int skip_rows_without) {
+                                                               int chunks, int skip_rows_without) {
   constexpr int NT = Terms<F16>::n;
   constexpr int HALVES = EPI == 1 ? 2 : 1;
+  constexpr int T = 16 * MI;
+  extern __shared__ f32x4 vs[];  // [T][rank / 4 rounded up to 8], 16-byte units swizzled by the row
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int64_t tile = blockIdx.x / (unsigned)col_blocks;
-  const int64_t m0 = tile * (16 * MI);
-  const int64_t width = EPI == 1 ? a.N / 2 : a.N;  // of out
-  const int64_t n0 = (int64_t)(blockIdx.x % (unsigned)col_blocks) * (64 * kWaves) + wave * 64;
-  if (n0 >= width) return;  // no barriers in this kernel
-  const int64_t n = n0 + 4 * r16;
-  const int id = tile_id<16 * MI>(a.row_adapter, m0, a.M, a.adapters, lane);
+  const int64_t m0 = (int64_t)(blockIdx.x / (unsigned)col_blocks) * T;
+  const int width = (int)(EPI == 1 ? a.N / 2 : a.N);  // of out
+  const int first = (int)(blockIdx.x % (unsigned)col_blocks) * chunks;
+  const int units = (a.rank + 31) / 32 * 8;
+  const int id = tile_id<T>(a.row_adapter, m0, a.M, a.adapters, lane);
+  bool again = false;
   each_adapter(id, skip_rows_without ? 0 : -1, blockIdx.y, slots, [&](int cur, uint64_t rows) {
     const int rank = adapter_rank(a, cur);
-    f32x4 acc[HALVES][MI][4];
-#pragma unroll
-    for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) acc[h][i][s] = f32x4{0.f, 0.f, 0.f, 0.f};
     const float scaling = cur >= 0 && a.scaling ? a.scaling[cur] : 1.0f;
-    for (int k0 = 0; k0 < rank; k0 += 32) {
+    const uint16_t *const b = a.b + (int64_t)cur * a.N * a.rank;
+
+    // B of columns n .. n + 3 of half h, ranks k0 + 8 g ..: as loaded, then as terms
+    auto load_b = [&](int n, int h, int k0, u32x4 (&raw)[4]) {
       const int k = k0 + g * 8;
-      bf16x8 bt[HALVES][4][NT];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        raw[s] = u32x4{0, 0, 0, 0};
+        const int64_t col = min(n + s, width - 1) + (int64_t)h * width;
+        if (k < rank) raw[s] = *reinterpret_cast<const u32x4 *>(b + col * a.rank + k);
+      }
+    };
+    auto mask_b = [&](int k0, u32x4 &raw) {
+      if (k0 + 32 <= rank) return;
+      // table entries past the adapter's own rank may hold anything
+      const int k = k0 + g * 8;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (k + 2 * e >= rank) raw[e] = 0;
+        else if (k + 2 * e + 1 >= rank) raw[e] &= 0xFFFFu;
+      }
+    };
+
+    // the streams of rows 16 i .., columns of chunk ch
+    Raw4<YT, VEC> y_raw[HALVES][4];
+    Raw4<OT, VEC> res_raw[4];
+    Raw4<F32, VEC> gate_raw;
+    u32x4 b_raw[HALVES][KB ? KB : 1][4];
+    auto column = [&](int ch) { return (first + ch) * (64 * kWaves) + wave * 64 + 4 * r16; };
+    auto live = [&](int i, int e) -> bool { return (rows >> (16 * i + 4 * g + e)) & 1; };
+    auto load_streams = [&](int ch, int i) {
+      const int64_t m = m0 + 16 * i;
+      const Tile<VEC> y = {column(ch), width, (int)a.N}, out = {column(ch), width, width};
+      const __amdgpu_buffer_rsrc_t y_buf = tile_buffer(a.y, m, a.N, sizeof(typename YT::type));
 #pragma unroll
       for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int64_t col = min(n + s, width - 1) + h * width;
-          u32x4 raw = {0, 0, 0, 0};
-          if (k < rank) raw = *reinterpret_cast<const u32x4 *>(a.b + ((int64_t)cur * a.N + col) * a.rank + k);
-          if (k0 + 32 > rank) {
-            // table entries past the adapter's own rank may hold anything
+        for (int e = 0; e < 4; ++e) y.template load<YT>(y_buf, 4 * g + e, h * width, live(i, e), y_raw[h][e]);
+      if constexpr (EPI == 2) {
+        const __amdgpu_buffer_rsrc_t res_buf = tile_buffer(a.residual, m, width, sizeof(typename OT::type));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (k + 2 * e >= rank) raw[e] = 0;
-              else if (k + 2 * e + 1 >= rank) raw[e] &= 0xFFFFu;
-            }
-          }
-          table_terms<F16>(raw, bt[h][s]);
-        }
+        for (int e = 0; e < 4; ++e) out.template load<OT>(res_buf, 4 * g + e, 0, live(i, e), res_raw[e]);
+        out.template load<F32>(tile_buffer(a.gate, (uint32_t)m / (uint32_t)a.gate_rows, width, 4), 0, 0, true, gate_raw);
+      }
+    };
+    auto load_table = [&](int ch) {
+      if constexpr (KB > 0) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int row = i * 16 + r16;
-        const int pick = (rows >> row) & 1 ? row : (int)__builtin_ctzll(rows);
-        float f[8];
+        for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = 0.f;
-        if (k < rank) {
-          const float *p = a.v + (m0 + pick) * a.rank + k;
-          F32::load8(p, 0, f);
-          for (int q = 1; q < splits; ++q) {
-            float o[8];
-            F32::load8(p + (int64_t)q * a.M * a.rank, 0, o);
+          for (int k = 0; k < KB; ++k) load_b(column(ch), h, 32 * k, b_raw[h][k]);
+      }
+    };
+
+    int i = -1, ch = 0;
+    auto next_group = [&](int after) -> int {  // the tile's next 16 rows with rows of this adapter
+      for (int j = after + 1; j < MI; ++j)
+        if ((rows >> (16 * j)) & 0xFFFF) return j;
+      return MI;
+    };
+    const int group0 = next_group(-1);
+    i = group0;
+    const bool any = first * (64 * kWaves) + wave * 64 < width;
+    if (any) {
+      load_table(0);
+      load_streams(0, i);
+    }
+    if (again) __syncthreads();  // the previous adapter's v has been read
+    again = true;
+    for (int u = threadIdx.x; u < T * units; u += 64 * kWaves) {
+      const int row = u / units, c = u % units;
+      f32x4 t = {0.f, 0.f, 0.f, 0.f};
+      if (((rows >> row) & 1) && 4 * c < rank) {
+        const float *p = a.v + (m0 + row) * a.rank + 4 * c;
+        const int64_t split = a.M * a.rank;
+        f32x4 part[kMostSplits];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] += o[e];
-          }
-        }
+        for (int q = 0; q < kMostSplits; ++q)
+          part[q] = q < splits ? *reinterpret_cast<const f32x4 *>(p + q * split) : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = k + e < rank ? f[e] * scaling : 0.f;
+        for (int q = 0; q < kMostSplits; ++q) t += part[q];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = 4 * c + e < rank ? t[e] * scaling : 0.f;
+      }
+      vs[row * units + (c ^ (row & 7))] = t;
+    }
+    __syncthreads();
+    if (!any) return;
+    for (;;) {
+      f32x4 acc[HALVES][4];
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) acc[h][s] = f32x4{0.f, 0.f, 0.f, 0.f};
+      auto step = [&](int k, const u32x4 (&raw)[HALVES][4]) {
+        const int row = 16 * i + r16, c = 8 * k + 2 * g;
+        const f32x4 lo = vs[row * units + (c ^ (row & 7))], hi = vs[row * units + ((c + 1) ^ (row & 7))];
+        const float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         bf16x8 vt[3];
         split3(f, vt);
 #pragma unroll
-        for (int t = 2; t >= 0; --t)
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            bf16x8 bt[NT];
+            u32x4 w = raw[h][s];
+            mask_b(32 * k, w);
+            table_terms<F16>(w, bt);
+#pragma unroll
+            for (int q = 2; q >= 0; --q)
+#pragma unroll
+              for (int p = 0; p < NT; ++p) acc[h][s] = mfma(vt[q], bt[p], acc[h][s]);
+          }
+      };
+      if constexpr (KB > 0) {
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+          u32x4 raw[HALVES][4];
 #pragma unroll
           for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+            for (int s = 0; s < 4; ++s) raw[h][s] = b_raw[h][k][s];
+          step(k, raw);
+        }
+      } else {
+        for (int k = 0; 32 * k < rank; ++k) {
+          u32x4 raw[HALVES][4];
 #pragma unroll
-              for (int q = 0; q < NT; ++q) acc[h][i][s] = mfma(vt[t], bt[h][s][q], acc[h][i][s]);
+          for (int h = 0; h < HALVES; ++h) load_b(column(ch), h, 32 * k, raw[h]);
+          step(k, raw);
+        }
       }
-    }
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
+      const Tile<VEC> out = {column(ch), width, width};
+      const uint32_t m32 = (uint32_t)m0 + 16 * i, gate0 = EPI == 2 ? m32 / (uint32_t)a.gate_rows : 0;
+      const bool one_gate = EPI != 2 || (m32 + 15) / (uint32_t)a.gate_rows == gate0;
+      float o[4][4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int row = i * 16 + g * 4 + e;
-        if (!((rows >> row) & 1)) continue;
-        const int64_t m = m0 + row;
-        float t[HALVES][4];
-        auto get = [&](auto type, const void *p, int64_t at, float (&f)[4]) {
-          using T = decltype(type);
-          if constexpr (VEC) {
-            if (n < width) T::load4(p, at, f);
-          } else {
+        float t[HALVES][4], res[4], gt[4];
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-              if (n + s < width) f[s] = T::load(p, at + s);
+        for (int h = 0; h < HALVES; ++h) unpack4<YT, VEC>(y_raw[h][e], t[h]);
+        if constexpr (EPI == 2) {
+          unpack4<OT, VEC>(res_raw[e], res);
+          if (one_gate) {
+            unpack4<F32, VEC>(gate_raw, gt);
+          } else {  // a boundary of samples among the 16 rows
+            const uint32_t at = m32 + 4 * g + e;
+            Raw4<F32, VEC> raw;
+            out.template load<F32>(tile_buffer(a.gate, gate0, width, 4), (int)(at / (uint32_t)a.gate_rows - gate0), 0,
+                                   live(i, e), raw);
+            unpack4<F32, VEC>(raw, gt);
           }
-        };
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
-          float base[4] = {0.f, 0.f, 0.f, 0.f};
-          if (a.y) get(YT{}, a.y, m * a.N + h * width + n, base);
-#pragma unroll
-          for (int s = 0; s < 4; ++s) t[h][s] = base[s] + acc[h][i][s][e];
         }
-        float o[4];
-        if constexpr (EPI == 1) {
 #pragma unroll
-          for (int s = 0; s < 4; ++s) o[s] = silu_mul(t[0][s], t[1][s]);
-        } else if constexpr (EPI == 2) {
-          float res[4] = {0.f, 0.f, 0.f, 0.f}, gt[4] = {0.f, 0.f, 0.f, 0.f};
-          get(OT{}, a.residual, m * width + n, res);
-          get(F32{}, a.gate, (int64_t)((uint64_t)m / (uint64_t)a.gate_rows) * width + n, gt);
-#pragma unroll
-          for (int s = 0; s < 4; ++s) o[s] = __builtin_fmaf(gt[s], t[0][s], res[s]);
-        } else {
-#pragma unroll
-          for (int s = 0; s < 4; ++s) o[s] = t[0][s];
-        }
-        if constexpr (VEC) {
-          if (n < width) OT::store4(a.out, m * width + n, o);
-        } else {
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            if (n + s < width) OT::store(a.out, m * width + n + s, o[s]);
+        for (int s = 0; s < 4; ++s) {
+          const float v = t[0][s] + acc[0][s][e];
+          if constexpr (EPI == 1) o[e][s] = silu_mul(v, t[HALVES - 1][s] + acc[HALVES - 1][s][e]);
+          else if constexpr (EPI == 2) o[e][s] = __builtin_fmaf(gt[s], v, res[s]);
+          else o[e][s] = v;
         }
       }
+      const __amdgpu_buffer_rsrc_t out_buf = tile_buffer(a.out, m0 + 16 * i, width, sizeof(typename OT::type));
+      bool keep[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) keep[e] = live(i, e);
+      i = next_group(i);
+      bool more = true;
+      if (i == MI) {
+        i = group0;
+        ++ch;
+        more = ch < chunks && (first + ch) * (64 * kWaves) + wave * 64 < width;
+        if (more) load_table(ch);
+      }
+      if (more) load_streams(ch, i);
+      __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the stores
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out.template store<OT>(out_buf, 4 * g + e, keep[e], o[e]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (!more) break;
+    }
   });
 }
 
-template <int MI, int RJ>
+template <int MI, int WR, int RJ>
 void launch_down(const AdapterArgs &a, const AdapterPlan &p, hipStream_t stream) {
   const int units = (int)(a.K / 64), per = (units + p.splits - 1) / p.splits;
   const int chunks = (a.rank + 16 * RJ - 1) / (16 * RJ);
   const dim3 grid((unsigned)p.tiles, (unsigned)p.splits, (unsigned)(p.slots * chunks)), block(64 * kWaves);
-  if (a.ab_f16) hipLaunchKernelGGL((adapter_down_kernel<MI, RJ, true>), grid, block, 0, stream, a, p.slots, per);
-  else hipLaunchKernelGGL((adapter_down_kernel<MI, RJ, false>), grid, block, 0, stream, a, p.slots, per);
+  if (a.ab_f16) hipLaunchKernelGGL((adapter_down_kernel<MI, WR, RJ, true, (MI > 1)>), grid, block, 0, stream, a, p.slots, per);
+  else hipLaunchKernelGGL((adapter_down_kernel<MI, WR, RJ, false, (MI > 1)>), grid, block, 0, stream, a, p.slots, per);
 }
 
+// 64-row tiles: two waves along the rows, or all four along K where a unit of
+// the table is as large as the rows' (every wave along the rows reads it again:
+// rank 64, 16896 x 12288 -> 4608 gated 266 us along K, 290 us with two and two;
+// rank 32, 4608 x 4608 -> 13824 126 and 123 us).
 template <int MI>
-void launch_down_mi(const AdapterArgs &a, const AdapterPlan &p, hipStream_t stream) {
-  if (a.rank <= 16) launch_down<MI, 1>(a, p, stream);
-  else if (a.rank <= 32) launch_down<MI, 2>(a, p, stream);
-  else launch_down<MI, 4>(a, p, stream);
+void launch_down_rank(const AdapterArgs &a, const AdapterPlan &p, hipStream_t stream) {
+  constexpr int HALF = MI == 4 ? 2 : 1;
+  if (a.rank <= 16) launch_down<MI / HALF, HALF, 1>(a, p, stream);
+  else if (a.rank <= 32) launch_down<MI / HALF, HALF, 2>(a, p, stream);
+  else launch_down<MI, 1, 4>(a, p, stream);
 }
 
 template <int MI, bool F16, typename YT, typename OT, int EPI>
 void launch_up(const AdapterArgs &a, const AdapterPlan &p, hipStream_t stream) {
   const int64_t width = EPI == 1 ? a.N / 2 : a.N;
-  const int col_blocks = (int)((width + 64 * kWaves - 1) / (64 * kWaves));
+  const int64_t blocks = (width + 64 * kWaves - 1) / (64 * kWaves);
+  const int chunks = (int)std::min<int64_t>(p.chunks, blocks);
+  const int col_blocks = (int)((blocks + chunks - 1) / chunks);
   const dim3 grid((unsigned)(p.tiles * col_blocks), (unsigned)p.slots), block(64 * kWaves);
+  const unsigned lds = (unsigned)(16 * MI * ((a.rank + 31) / 32 * 32) * 4);  // 64 KB at most
   // without an epilogue a row without an adapter is a copy of y, which is
   // nothing to do in place
   const int skip = EPI == 0 && a.y == a.out;
-  if (a.vec) hipLaunchKernelGGL((adapter_up_kernel<MI, F16, YT, OT, EPI, true>), grid, block, 0, stream, a, p.slots, p.splits, col_blocks, skip);
-  else hipLaunchKernelGGL((adapter_up_kernel<MI, F16, YT, OT, EPI, false>), grid, block, 0, stream, a, p.slots, p.splits, col_blocks, skip);
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, lds, stream, a, p.slots, p.splits, col_blocks, chunks, skip);
+  };
+  if (!a.vec) run(adapter_up_kernel<MI, 0, F16, YT, OT, EPI, false>);
+  else if (a.rank <= 32) run(adapter_up_kernel<MI, 1, F16, YT, OT, EPI, true>);
+  else if (a.rank <= 64) run(adapter_up_kernel<MI, 2, F16, YT, OT, EPI, true>);
+  else run(adapter_up_kernel<MI, 0, F16, YT, OT, EPI, true>);
 }
 
 template <int MI, bool F16, typename YT, typename OT>
@@ -375,7 +573,7 @@ void launch_up_types(const AdapterArgs &a, const AdapterPlan &p, hipStream_t str
 
 template <int MI>
 hipError_t launch_mi(const AdapterArgs &a, const AdapterPlan &p, hipStream_t stream) {
-  if (a.adapters > 0) launch_down_mi<MI>(a, p, stream);
+  if (a.adapters > 0) launch_down_rank<MI>(a, p, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.ab_f16) launch_up_types<MI, true>(a, p, stream);
@@ -387,20 +585,37 @@ hipError_t launch_mi(const AdapterArgs &a, const AdapterPlan &p, hipStream_t str
 
 AdapterPlan adapter_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t adapters) {
   AdapterPlan p{};
-  (void)N;
-  p.row_tile = M <= 256 ? 16 : 64;
+  // 16-row tiles up to 1024 rows: more blocks, and fewer adapters to a tile of
+  // short requests (512 rows of 16 requests, 4608 -> 4608 at rank 16: 16.3 us,
+  // with 64-row tiles 20.4; 1024 rows of 8 at rank 32: 21.8 and 24.5)
+  p.row_tile = M <= 1024 ? 16 : 64;
   p.tiles = (M + p.row_tile - 1) / p.row_tile;
-  // few tiles: blocks of their own for the adapters of one tile
+  // Few tiles: blocks of their own for the adapters of one tile, 128 over all
+  // tiles (203 rows of 14 requests: 11.1 us, at 32 over all 16.5; 256 rows of
+  // 64 adapters in turn 59 and 87)
   const int64_t distinct = std::min<int64_t>({M, (int64_t)p.row_tile, adapters + 1});
-  p.slots = (int)std::min<int64_t>(distinct, std::max<int64_t>(1, 32 / p.tiles));
-  const int chunk = rank <= 16 ? 16 : rank <= 32 ? 32 : 64;
-  const int64_t blocks = p.tiles * p.slots * ((rank + chunk - 1) / chunk);
+  p.slots = (int)std::min<int64_t>(distinct, std::max<int64_t>(1, (p.row_tile == 16 ? 128 : 1) / p.tiles));
+  // K ranges of the first launch: the count that takes the fewest rounds of
+  // 64-wide units per wave, each block costing about two units more than it
+  // has (its start, and its partial sums written and read)
+  const int rj = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
+  const int along_k = p.row_tile == 16 || rj == 4 ? kWaves : kWaves / 2;  // waves of a block
+  const int per_cu = p.row_tile == 16 ? 8 : rj == 1 ? 5 : rj == 2 ? 4 : 2;  // blocks, by their registers
+  const int64_t blocks = p.tiles * p.slots * ((rank + 16 * rj - 1) / (16 * rj)), held = (int64_t)kCus * per_cu;
   const int64_t units = K / 64;
-  int64_t splits = std::min<int64_t>({16, (units + kWaves - 1) / kWaves, (512 + blocks - 1) / blocks});
-  splits = std::max<int64_t>(splits, 1);
-  // no empty range
-  const int64_t per = std::max<int64_t>((units + splits - 1) / splits, 1);
-  p.splits = (int)std::max<int64_t>((units + per - 1) / per, 1);
+  const int most = p.row_tile == 16 ? kMostSplits : 6;
+  int64_t best = INT64_MAX;
+  p.splits = 1;
+  for (int64_t n = 1; n <= most && n <= std::max<int64_t>(units, 1); ++n) {
+    const int64_t per = (units + n - 1) / n;
+    if (n > 1 && (units + per - 1) / per != n) continue;  // an empty range
+    const int64_t cost = (blocks * n + held - 1) / held * ((per + along_k - 1) / along_k + 2);
+    if (cost < best) best = cost, p.splits = (int)n;
+  }
+  // columns of a block of the second launch: 512 where 256 leave plenty of
+  // blocks, so that v is summed less often (SwiGLU case 105 -> 96 us)
+  const int64_t cols = p.tiles * p.slots * ((N + 64 * kWaves - 1) / (64 * kWaves));
+  p.chunks = cols >= 2048 ? 2 : 1;
   return p;
 }
 

@@ -895,6 +895,7 @@ bool norm_ok(int kind, float eps) {
 
 constexpr int64_t kMaxNormRow = 65536;  // 16 waves of 64 lanes, 64 values each
 constexpr int64_t kMaxAdapterRank = 256;
+constexpr int64_t kMaxAdapterColumns = int64_t(1) << 22;  // 64 rows of bf16 (K) or 16 of fp32 (N) within a 31-bit offset
 constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / 256 - 1;  // a grid holds fewer than 2^32 threads
 constexpr int64_t kMaxNormBlocks = (int64_t(1) << 32) / 1024 - 1;
 
@@ -972,14 +973,16 @@ QL_API int qlinear_block_norm(const ql_block_norm_args *a, void *stream) {
 }
 
 QL_API size_t qlinear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters) {
-  if (!adapter_sizes_ok(M, N, K, adapters) || !adapter_rank_ok(rank) || M == 0 || N == 0) return 0;
+  if (!adapter_sizes_ok(M, N, K, adapters) || !adapter_rank_ok(rank) || N > kMaxAdapterColumns || K > kMaxAdapterColumns || M == 0 ||
+      N == 0)
+    return 0;
   return adapter_ws(ql::adapter_plan(M, N, K, (int)rank, adapters), M, rank, adapters);
 }
 
 QL_API int qlinear_adapters(const ql_adapter_args *a, void *stream) {
   if (!a) return QL_EINVAL;
   if (!adapter_sizes_ok(a->M, a->N, a->K, a->adapters)) return QL_EINVAL;
-  if (!adapter_rank_ok(a->rank)) return QL_EUNSUPPORTED;
+  if (!adapter_rank_ok(a->rank) || a->N > kMaxAdapterColumns || a->K > kMaxAdapterColumns) return QL_EUNSUPPORTED;
   if (a->ab_dtype != QL_ADAPTER_BF16 && a->ab_dtype != QL_ADAPTER_F16) return QL_EINVAL;
   if (!dtype_ok(a->out_dtype) || (a->y && !dtype_ok(a->y_dtype))) return QL_EINVAL;
   if (a->epilogue != QL_EPI_NONE && a->epilogue != QL_EPI_SWIGLU && a->epilogue != QL_EPI_GATE_RESIDUAL) return QL_EINVAL;

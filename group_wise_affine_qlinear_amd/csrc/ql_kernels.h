@@ -190,6 +190,7 @@ struct AdapterPlan {
   int row_tile;    // rows per block
   int slots;       // blocks that share the adapters of one row tile
   int splits;      // K ranges, fp32 partials in the workspace
+  int chunks;      // 256-column pieces per block of the second launch
   int64_t tiles;
 };
 AdapterPlan adapter_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t adapters);

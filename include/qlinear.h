@@ -540,7 +540,7 @@ typedef struct ql_adapter_args {
  * Returns QL_EINVAL for bad sizes, types or missing arrays, QL_EALIGN if x, a,
  * b or the workspace is not 16-byte aligned or another pointer is not aligned
  * to its element, QL_EUNSUPPORTED for a rank that is not a multiple of 8 up to
- * 256, QL_EWORKSPACE for a missing or too small workspace. M == 0 or N == 0 is
+ * 256 or N or K above 2^22, QL_EWORKSPACE for a missing or too small workspace. M == 0 or N == 0 is
  * a no-op. Calls that share one workspace must not overlap in time; nothing
  * in it is kept from one call to the next. No allocation, no synchronization.
  */

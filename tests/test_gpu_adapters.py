@@ -126,6 +126,9 @@ SIZES = [
     (16, 256, 320, 32, 20), (17, 257, 512, 40, 5), (63, 255, 64, 64, 7), (64, 512, 640, 72, 64), (65, 1003, 448, 128, 3),
     (130, 64, 1024, 256, 9), (255, 36, 2048, 16, 1), (256, 260, 128, 8, 40), (257, 300, 576, 16, 6), (300, 1001, 64, 48, 2),
     (321, 130, 4608, 136, 5), (640, 512, 832, 64, 11), (1000, 96, 256, 32, 3), (33, 8, 12288, 16, 2),
+    # more than 1024 rows: 64-row tiles
+    (1025, 64, 64, 8, 1), (1030, 260, 192, 64, 5), (1100, 67, 320, 136, 9), (1500, 128, 128, 16, 70), (1091, 512, 704, 24, 3),
+    (2100, 36, 1024, 256, 2), (1200, 300, 2048, 48, 4), (1063, 1000, 320, 32, 12),
 ]
 
 
@@ -142,13 +145,13 @@ def test_sizes(torch, M, N, K, rank, n, ids):
 @pytest.mark.parametrize("table", ["bf16", "f16"])
 @pytest.mark.parametrize("y", ["f32", "bf16", None])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-@pytest.mark.parametrize("M,N", [(21, 264), (300, 262), (9, 130)])
+@pytest.mark.parametrize("M,N", [(21, 264), (300, 262), (9, 130), (1061, 264), (1030, 130)])
 def test_types_and_epilogues(torch, epilogue, table, y, out, M, N):
     p = Problem(torch, M, N, 192, 40, 5, ids="mixed", y=y, out=out, table=table, epilogue=epilogue)
     p.check(p.call())
 
 
-@pytest.mark.parametrize("M", [5, 40, 400])
+@pytest.mark.parametrize("M", [5, 40, 400, 1100])
 def test_ranks_of_their_own(torch, M):
     """Odd ranks, a rank of zero, ranks below and beyond the table's (clamped); what the table holds past an
     adapter's rank does not matter."""
@@ -164,7 +167,7 @@ def test_ranks_of_their_own(torch, M):
         assert torch.equal(p.call(), first)
 
 
-@pytest.mark.parametrize("M", [1, 16, 300])
+@pytest.mark.parametrize("M", [1, 16, 300, 1033])
 def test_no_adapter_at_all(torch, M):
     for ids in (-1, 3, 2 ** 31 - 1, -2 ** 31):
         p = Problem(torch, M, 70, 64, 8, 3, ids=[ids] * M)
@@ -186,7 +189,7 @@ def test_k_of_zero(torch):
     assert torch.equal(p.call(), p.y)
 
 
-@pytest.mark.parametrize("M", [16, 37, 300])
+@pytest.mark.parametrize("M", [16, 37, 300, 1033])
 def test_rows_without_an_adapter_stay_in_place(torch, M):
     p = Problem(torch, M, 200, 128, 16, 4, ids="mixed")
     ids = p.ids.cpu()
@@ -202,8 +205,9 @@ def test_rows_without_an_adapter_stay_in_place(torch, M):
 
 @pytest.mark.parametrize("epilogue", ["none", "gate"])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-def test_in_place(torch, epilogue, dt):
-    p = Problem(torch, 90, 260, 320, 24, 6, y=dt, out=dt, epilogue=epilogue)
+@pytest.mark.parametrize("M", [90, 1210])
+def test_in_place(torch, epilogue, dt, M):
+    p = Problem(torch, M, 260, 320, 24, 6, y=dt, out=dt, epilogue=epilogue)
     apart = p.call()
     out = p.y.clone()
     assert torch.equal(p.call(out, y=out), apart)
@@ -212,7 +216,7 @@ def test_in_place(torch, epilogue, dt):
         assert torch.equal(p.call(stream, residual=stream), apart)
 
 
-@pytest.mark.parametrize("M", [14, 200, 300])
+@pytest.mark.parametrize("M", [14, 200, 300, 1100])
 def test_what_others_hold_never_reaches_a_row(torch, M):
     """NaN and infinities in the rows of one request, in its adapter's tables, and in rows without an adapter."""
     p = Problem(torch, M, 132, 320, 24, 5, ids="mixed")
@@ -232,7 +236,7 @@ def test_what_others_hold_never_reaches_a_row(torch, M):
             assert not bool(torch.isfinite(out[other]).any())
 
 
-@pytest.mark.parametrize("M", [16, 150, 320])
+@pytest.mark.parametrize("M", [16, 150, 320, 1090])
 def test_a_row_does_not_depend_on_its_place(torch, M):
     """The same rows in another order give the same bits, each at its new place."""
     p = Problem(torch, M, 260, 960, 40, 6, ids="mixed")
@@ -332,7 +336,7 @@ def test_two_graphs_share_a_workspace(torch):
 
 
 def test_two_streams(torch):
-    ps = [Problem(torch, 500, 1024, 1024, 32, 4, seed=s) for s in (1, 2)]
+    ps = [Problem(torch, 1500, 1024, 1024, 32, 4, seed=s) for s in (1, 2)]
     want = [p.call() for p in ps]
     streams = [torch.cuda.Stream() for _ in ps]
     outs = [torch.empty_like(w) for w in want]
