@@ -112,21 +112,27 @@ __device__ __forceinline__ int adapter_rank(const AdapterArgs &a, int id) {
 
 // v = A x over a range of K. Block: WR*MI*16 rows, RJ*16 ranks; its waves are
 // WR along the rows, and the others take the range's 64-wide K units in turn
-// and add their sums in LDS in wave order. A lane's 32 bytes of a row (two
-// MFMA steps) lie side by side, so the four lanes of a row read its whole
-// 128-byte line. With DOUBLE a wave requests its next unit before it
-// multiplies the one it has: at 64-row tiles that is worth more than the waves
-// its registers cost (SwiGLU case of 4096 rows 97 -> 90 us in all); at 16-row
-// tiles, where a wave has one to three units, it is not (10.7 -> 10.8 us).
-template <int MI, int WR, int RJ, bool F16, bool DOUBLE>
+// and add their sums in LDS in wave order.
+//
+// A unit of rows is loaded eight 128-byte lines to an instruction, eight
+// neighbouring lanes to a line, and turned into MFMA operands (16 rows to 16
+// neighbouring lanes) in LDS of the wave's own, without a barrier: loads in
+// operand order, 16 bytes of 16 rows to neighbouring lanes, run at 15 B/clk
+// and CU from L2, loads by lines at 45 to 57 (a 64 x 4608 table read by every
+// CU). Line r keeps its 16-byte piece c at c ^ (r & 7): no bank conflicts.
+// The next unit is requested before this one is multiplied.
+template <int MI, int WR, int RJ, bool F16>
 __global__ __launch_bounds__(64 * kWaves) void adapter_down_kernel(AdapterArgs a, int slots, int units_per_split) {
   constexpr int NT = Terms<F16>::n;
   constexpr int T = 16 * MI * WR, KW = kWaves / WR;
-  __shared__ f32x4 red[KW - 1][WR][MI * RJ][64];
+  constexpr int LINES = 16 * (MI + RJ);            // of one unit: x, then the table
+  constexpr int SUMS = (KW - 1) * WR * MI * RJ * 64;  // 16-byte words of the waves' sums
+  __shared__ f32x4 lds[SUMS > kWaves * LINES * 8 ? SUMS : kWaves * LINES * 8];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave % WR, wk = wave / WR;
   const int r16 = lane & 15, g = lane >> 4;
+  u32x4 *const stage = reinterpret_cast<u32x4 *>(lds) + wave * LINES * 8;
   const int64_t m0 = (int64_t)blockIdx.x * T;
   const int slot = blockIdx.z % slots;
   const int r0 = (int)(blockIdx.z / slots) * (16 * RJ);
@@ -136,93 +142,85 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_down_kernel(AdapterArgs a
   each_adapter(id, 0, slot, slots, [&](int cur, uint64_t rows) {
     const int rank = adapter_rank(a, cur);
     if (r0 >= rank) return;
-    // rows of x and of the table as offsets into the tile's and the adapter's part
+    // lines of x and of the table as offsets into the tile's and the adapter's part
     const __amdgpu_buffer_rsrc_t x_buf = make_rsrc(a.x, m0 * a.K * 2, INT32_MAX);
     const __amdgpu_buffer_rsrc_t a_buf = make_rsrc(a.a, ((int64_t)cur * a.rank + r0) * a.K * 2, INT32_MAX);
     const int first = wr * (16 * MI);
-    int x_at[MI], a_at[RJ];
+    int x_at[2 * MI], a_at[2 * RJ];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int row = first + i * 16 + r16;
+    for (int i = 0; i < 2 * MI; ++i) {
+      const int row = first + i * 8 + (lane >> 3);
       const int pick = (rows >> row) & 1 ? row : (int)__builtin_ctzll(rows);  // rows of others: not loaded
-      x_at[i] = pick * (int)a.K * 2 + g * 32;
+      x_at[i] = pick * (int)a.K * 2 + (lane & 7) * 16;
     }
 #pragma unroll
-    for (int j = 0; j < RJ; ++j) a_at[j] = min(j * 16 + r16, rank - r0 - 1) * (int)a.K * 2 + g * 32;
+    for (int j = 0; j < 2 * RJ; ++j) a_at[j] = min(j * 8 + (lane >> 3), rank - r0 - 1) * (int)a.K * 2 + (lane & 7) * 16;
     f32x4 acc[MI][RJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < RJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    struct Unit {
-      u32x4 x[MI][2], a[RJ][2];
-    } one, two;
-    auto load = [&](int u, Unit &t) {
+    u32x4 line[2 * (MI + RJ)];
+    auto load = [&](int u) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int i = 0; i < 2 * MI; ++i)
+        line[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x_buf, x_at[i], u * 128, 0));
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          t.x[i][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x_buf, x_at[i] + s * 16, u * 128, 0));
-#pragma unroll
-      for (int j = 0; j < RJ; ++j)
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-          t.a[j][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(a_buf, a_at[j] + s * 16, u * 128, 0));
-      if constexpr (DOUBLE) __builtin_amdgcn_sched_barrier(0);  // requested before the other unit is worked on
+      for (int j = 0; j < 2 * RJ; ++j)
+        line[2 * MI + j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(a_buf, a_at[j], u * 128, 0));
     };
-    auto multiply = [&](const Unit &t) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < RJ; ++j) {
-          bf16x8 w[NT];
-          table_terms<F16>(t.a[j][s], w);
-#pragma unroll
-          for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int k = 0; k < NT; ++k) acc[i][j] = mfma(w[k], as_bf16x8(t.x[i][s]), acc[i][j]);
-        }
-      if constexpr (DOUBLE) __builtin_amdgcn_sched_barrier(0);
+    const int put = (lane >> 3) * 8 + ((lane & 7) ^ (lane >> 3));
+    auto operand = [&](int tile, int s) {  // 16 lines from 16 * tile, the 16-byte piece 2 g + s
+      return stage[(tile * 16 + r16) * 8 + ((2 * g + s) ^ (r16 & 7))];
     };
-    const int last = u1 - 1;
     if (((rows >> first) & (~0ull >> (64 - 16 * MI))) != 0 && u0 + wk < u1) {
-      if constexpr (DOUBLE) {
-        load(u0 + wk, one);
-        for (int u = u0 + wk; u < u1; u += 2 * KW) {
-          load(min(u + KW, last), two);
-          multiply(one);
-          load(min(u + 2 * KW, last), one);
-          if (u + KW < u1) multiply(two);
-        }
-      } else {
-        for (int u = u0 + wk; u < u1; u += KW) {
-          load(u, one);
-          multiply(one);
+      load(u0 + wk);
+      for (int u = u0 + wk; u < u1; u += KW) {
+#pragma unroll
+        for (int i = 0; i < 2 * (MI + RJ); ++i) stage[i * 64 + put] = line[i];
+        load(min(u + KW, u1 - 1));
+        __builtin_amdgcn_sched_barrier(0);  // requested before the products
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          bf16x8 x[MI];
+#pragma unroll
+          for (int i = 0; i < MI; ++i) x[i] = as_bf16x8(operand(i, s));
+#pragma unroll
+          for (int j = 0; j < RJ; ++j) {
+            bf16x8 w[NT];
+            table_terms<F16>(operand(MI + j, s), w);
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+              for (int k = 0; k < NT; ++k) acc[i][j] = mfma(w[k], x[i], acc[i][j]);
+          }
         }
       }
     }
-    __syncthreads();  // the previous adapter's sums have been read
+    __syncthreads();  // every wave's operands, and the previous adapter's sums, have been read
     if (wk > 0) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < RJ; ++j) red[wk - 1][wr][i * RJ + j][lane] = acc[i][j];
+        for (int j = 0; j < RJ; ++j) lds[(((wk - 1) * WR + wr) * (MI * RJ) + i * RJ + j) * 64 + lane] = acc[i][j];
     }
     __syncthreads();
-    if (wk > 0) return;
-    float *v = a.v + (int64_t)blockIdx.y * a.M * a.rank;
+    if (wk == 0) {
+      float *v = a.v + (int64_t)blockIdx.y * a.M * a.rank;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int row = first + i * 16 + r16;
+      for (int i = 0; i < MI; ++i) {
+        const int row = first + i * 16 + r16;
 #pragma unroll
-      for (int j = 0; j < RJ; ++j) {
-        f32x4 t = acc[i][j];
+        for (int j = 0; j < RJ; ++j) {
+          f32x4 t = acc[i][j];
 #pragma unroll
-        for (int w = 0; w < KW - 1; ++w) t += red[w][wr][i * RJ + j][lane];
-        const int r = r0 + j * 16 + g * 4;
-        if (((rows >> row) & 1) && r < a.rank) *reinterpret_cast<f32x4 *>(v + (m0 + row) * a.rank + r) = t;
+          for (int w = 0; w < KW - 1; ++w) t += lds[((w * WR + wr) * (MI * RJ) + i * RJ + j) * 64 + lane];
+          const int r = r0 + j * 16 + g * 4;
+          if (((rows >> row) & 1) && r < a.rank) *reinterpret_cast<f32x4 *>(v + (m0 + row) * a.rank + r) = t;
+        }
       }
     }
+    __syncthreads();  // the sums have been read: the next adapter's operands may take their place
   });
 }
 
@@ -331,15 +329,33 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
     const float scaling = cur >= 0 && a.scaling ? a.scaling[cur] : 1.0f;
     const uint16_t *const b = a.b + (int64_t)cur * a.N * a.rank;
 
-    // B of columns n .. n + 3 of half h, ranks k0 + 8 g ..: as loaded, then as terms
-    auto load_b = [&](int n, int h, int k0, u32x4 (&raw)[4]) {
-      const int k = k0 + g * 8;
+    // B of the wave's 64 columns from n0 of half h, ranks k0 .. k0 + 31: rows
+    // (columns of out) 4 r16 + s, ranks 8 g .. 8 g + 7 of subtile s. With TURN,
+    // where it is read for every step, it is loaded four neighbouring lanes to
+    // a row's 64 bytes and turned in LDS of the wave's own: in operand order
+    // neighbouring lanes are 4 rows apart, and such loads run at a quarter of
+    // the rate (SwiGLU 2048 x 4608 -> 24576 at rank 128: 202 -> 147 us). Read
+    // once for four steps it is not worth the LDS (rank 16: 90 -> 96 us).
+    constexpr bool TURN = KB == 0;
+    u32x4 *const stage = reinterpret_cast<u32x4 *>(vs + T * units) + wave * 256;
+    auto load_b = [&](int n0, int h, int k0, u32x4 (&raw)[4]) {
+      const int k = k0 + (TURN ? lane & 3 : g) * 8;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        raw[s] = u32x4{0, 0, 0, 0};
-        const int64_t col = min(n + s, width - 1) + (int64_t)h * width;
-        if (k < rank) raw[s] = *reinterpret_cast<const u32x4 *>(b + col * a.rank + k);
+      for (int q = 0; q < 4; ++q) {
+        raw[q] = u32x4{0, 0, 0, 0};
+        const int row = TURN ? q * 16 + (lane >> 2) : 4 * r16 + q;
+        const int64_t col = min(n0 + row, width - 1) + (int64_t)h * width;
+        if (k < rank) raw[q] = *reinterpret_cast<const u32x4 *>(b + col * a.rank + k);
       }
+    };
+    auto turn = [&](u32x4 (&raw)[4]) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = q * 4 + (lane >> 4), s = (lane >> 2) & 3;
+        stage[(s * 16 + row) * 4 + ((lane & 3) ^ (row & 3))] = raw[q];
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) raw[s] = stage[(s * 16 + r16) * 4 + (g ^ (r16 & 3))];
     };
     auto mask_b = [&](int k0, u32x4 &raw) {
       if (k0 + 32 <= rank) return;
@@ -357,7 +373,8 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
     Raw4<OT, VEC> res_raw[4];
     Raw4<F32, VEC> gate_raw;
     u32x4 b_raw[HALVES][KB ? KB : 1][4];
-    auto column = [&](int ch) { return (first + ch) * (64 * kWaves) + wave * 64 + 4 * r16; };
+    auto wave_column = [&](int ch) { return (first + ch) * (64 * kWaves) + wave * 64; };
+    auto column = [&](int ch) { return wave_column(ch) + 4 * r16; };
     auto live = [&](int i, int e) -> bool { return (rows >> (16 * i + 4 * g + e)) & 1; };
     auto load_streams = [&](int ch, int i) {
       const int64_t m = m0 + 16 * i;
@@ -379,7 +396,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
 #pragma unroll
         for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-          for (int k = 0; k < KB; ++k) load_b(column(ch), h, 32 * k, b_raw[h][k]);
+          for (int k = 0; k < KB; ++k) load_b(wave_column(ch), h, 32 * k, b_raw[h][k]);
       }
     };
 
@@ -454,11 +471,20 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
           step(k, raw);
         }
       } else {
-        for (int k = 0; 32 * k < rank; ++k) {
-          u32x4 raw[HALVES][4];
+        // one step of ranks ahead
+        u32x4 now[HALVES][4], ahead[HALVES][4];
 #pragma unroll
-          for (int h = 0; h < HALVES; ++h) load_b(column(ch), h, 32 * k, raw[h]);
-          step(k, raw);
+        for (int h = 0; h < HALVES; ++h) load_b(wave_column(ch), h, 0, now[h]);
+        for (int k = 0; 32 * k < rank; ++k) {
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) load_b(wave_column(ch), h, min(32 * k + 32, 32 * (units / 8 - 1)), ahead[h]);
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) turn(now[h]);
+          step(k, now);
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) now[h][s] = ahead[h][s];
         }
       }
       const Tile<VEC> out = {column(ch), width, width};
@@ -517,8 +543,8 @@ void launch_down(const AdapterArgs &a, const AdapterPlan &p, hipStream_t stream)
   const int units = (int)(a.K / 64), per = (units + p.splits - 1) / p.splits;
   const int chunks = (a.rank + 16 * RJ - 1) / (16 * RJ);
   const dim3 grid((unsigned)p.tiles, (unsigned)p.splits, (unsigned)(p.slots * chunks)), block(64 * kWaves);
-  if (a.ab_f16) hipLaunchKernelGGL((adapter_down_kernel<MI, WR, RJ, true, (MI > 1)>), grid, block, 0, stream, a, p.slots, per);
-  else hipLaunchKernelGGL((adapter_down_kernel<MI, WR, RJ, false, (MI > 1)>), grid, block, 0, stream, a, p.slots, per);
+  if (a.ab_f16) hipLaunchKernelGGL((adapter_down_kernel<MI, WR, RJ, true>), grid, block, 0, stream, a, p.slots, per);
+  else hipLaunchKernelGGL((adapter_down_kernel<MI, WR, RJ, false>), grid, block, 0, stream, a, p.slots, per);
 }
 
 // 64-row tiles: two waves along the rows, or all four along K where a unit of
@@ -540,17 +566,23 @@ void launch_up(const AdapterArgs &a, const AdapterPlan &p, hipStream_t stream) {
   const int chunks = (int)std::min<int64_t>(p.chunks, blocks);
   const int col_blocks = (int)((blocks + chunks - 1) / chunks);
   const dim3 grid((unsigned)(p.tiles * col_blocks), (unsigned)p.slots), block(64 * kWaves);
-  const unsigned lds = (unsigned)(16 * MI * ((a.rank + 31) / 32 * 32) * 4);  // 64 KB at most
   // without an epilogue a row without an adapter is a copy of y, which is
   // nothing to do in place
   const int skip = EPI == 0 && a.y == a.out;
-  const auto run = [&](auto kernel) {
+  const unsigned v_bytes = (unsigned)(16 * MI * ((a.rank + 31) / 32 * 32) * 4);  // v of the tile, 64 KB at most
+  const auto run = [&](auto kernel, unsigned turn_bytes) {
+    const unsigned lds = v_bytes + turn_bytes;
+    if (lds > 65536u && hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                            (int)lds) != hipSuccess)
+      return;  // reported by the check after the launches
     hipLaunchKernelGGL(kernel, grid, block, lds, stream, a, p.slots, p.splits, col_blocks, chunks, skip);
   };
-  if (!a.vec) run(adapter_up_kernel<MI, 0, F16, YT, OT, EPI, false>);
-  else if (a.rank <= 32) run(adapter_up_kernel<MI, 1, F16, YT, OT, EPI, true>);
-  else if (a.rank <= 64) run(adapter_up_kernel<MI, 2, F16, YT, OT, EPI, true>);
-  else run(adapter_up_kernel<MI, 0, F16, YT, OT, EPI, true>);
+  constexpr unsigned turn = kWaves * 4096;
+  if (!a.vec) run(adapter_up_kernel<MI, 0, F16, YT, OT, EPI, false>, turn);
+  else if (a.rank <= 32) run(adapter_up_kernel<MI, 1, F16, YT, OT, EPI, true>, 0);
+  else if (a.rank <= 64) run(adapter_up_kernel<MI, 2, F16, YT, OT, EPI, true>, 0);
+  else if (EPI != 1 && a.rank <= 128) run(adapter_up_kernel<MI, EPI != 1 ? 4 : 0, F16, YT, OT, EPI, true>, 0);
+  else run(adapter_up_kernel<MI, 0, F16, YT, OT, EPI, true>, turn);
 }
 
 template <int MI, bool F16, typename YT, typename OT>
@@ -595,27 +627,30 @@ AdapterPlan adapter_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t adap
   // 64 adapters in turn 59 and 87)
   const int64_t distinct = std::min<int64_t>({M, (int64_t)p.row_tile, adapters + 1});
   p.slots = (int)std::min<int64_t>(distinct, std::max<int64_t>(1, (p.row_tile == 16 ? 128 : 1) / p.tiles));
-  // K ranges of the first launch: the count that takes the fewest rounds of
-  // 64-wide units per wave, each block costing about two units more than it
-  // has (its start, and its partial sums written and read)
-  const int rj = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
-  const int along_k = p.row_tile == 16 || rj == 4 ? kWaves : kWaves / 2;  // waves of a block
-  const int per_cu = p.row_tile == 16 ? 8 : rj == 1 ? 5 : rj == 2 ? 4 : 2;  // blocks, by their registers
-  const int64_t blocks = p.tiles * p.slots * ((rank + 16 * rj - 1) / (16 * rj)), held = (int64_t)kCus * per_cu;
-  const int64_t units = K / 64;
-  const int most = p.row_tile == 16 ? kMostSplits : 6;
-  int64_t best = INT64_MAX;
-  p.splits = 1;
-  for (int64_t n = 1; n <= most && n <= std::max<int64_t>(units, 1); ++n) {
-    const int64_t per = (units + n - 1) / n;
-    if (n > 1 && (units + per - 1) / per != n) continue;  // an empty range
-    const int64_t cost = (blocks * n + held - 1) / held * ((per + along_k - 1) / along_k + 2);
-    if (cost < best) best = cost, p.splits = (int)n;
-  }
   // columns of a block of the second launch: 512 where 256 leave plenty of
   // blocks, so that v is summed less often (SwiGLU case 105 -> 96 us)
-  const int64_t cols = p.tiles * p.slots * ((N + 64 * kWaves - 1) / (64 * kWaves));
-  p.chunks = cols >= 2048 ? 2 : 1;
+  const int64_t col_blocks = (N + 64 * kWaves - 1) / (64 * kWaves);
+  p.chunks = p.tiles * p.slots * col_blocks >= 2048 ? 2 : 1;
+  // K ranges of the first launch, by its time and the second's: about 1 us for
+  // each 64-wide unit of a wave and 2 us to start, in as many rounds as the
+  // blocks need, and 1 ns for every 16 KB of partial sums, which are
+  // written once and read by every block of columns. Measured in all: rank 64,
+  // 4096 x 4608 -> 4608: 57.6, 46.6, 44.1, 43.5 us at 1, 2, 3, 4 ranges and
+  // 46.8 at 8; rank 16, 1 row: 10.3 us at 1, 8.9 at 2, 8.3 at 8.
+  const int rj = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
+  const int along_k = p.row_tile == 16 || rj == 4 ? kWaves : kWaves / 2;  // waves of a block
+  const int per_cu = p.row_tile == 16 ? (rj == 1 ? 8 : 4) : rj == 1 ? 5 : rj == 2 ? 4 : 2;  // blocks, by their registers
+  const int64_t blocks = p.tiles * p.slots * ((rank + 16 * rj - 1) / (16 * rj)), held = (int64_t)kCus * per_cu;
+  const int64_t units = K / 64;
+  const int64_t partial = M * rank * ((col_blocks + p.chunks - 1) / p.chunks + 2) / 4096;
+  int64_t best = INT64_MAX;
+  p.splits = 1;
+  for (int64_t n = 1; n <= kMostSplits && n <= std::max<int64_t>(units, 1); ++n) {
+    const int64_t per = (units + n - 1) / n;
+    if (n > 1 && (units + per - 1) / per != n) continue;  // an empty range
+    const int64_t cost = (blocks * n + held - 1) / held * ((per + along_k - 1) / along_k * 1000 + 2000) + n * partial;
+    if (cost < best) best = cost, p.splits = (int)n;
+  }
   return p;
 }
 

@@ -533,39 +533,44 @@ def _operand(t, name, dtypes, shape, device):
     raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _value_dtype(t, name):
+def _value_dtype(torch, t, name):
     """ql_out_dtype of a stream of values."""
-    torch = _torch()
-    if t.dtype == torch.float32:
+    dtype = t.dtype
+    if dtype is torch.float32:
         return QL_OUT_F32
-    if t.dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return QL_OUT_BF16
     raise TypeError(f"{name} must be float32 or bfloat16")
 
 
-def _modulation(t, name, rows, D, device):
+def _modulation(torch, t, name, rows, D, device):
     """(pointer, row pitch) of a [samples, D] fp32 tensor whose rows may be slices of longer ones."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
         raise TypeError(f"{name} must be a float32 tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != 2 or t.shape[1] != D or t.shape[0] < rows:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [>= {rows}, {D}]")
-    if (D > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < D):
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != D or shape[0] < rows:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [>= {rows}, {D}]")
+    pitch, step = t.stride()
+    if (D > 1 and step != 1) or (shape[0] > 1 and pitch < D):
         raise ValueError(f"{name} must have rows of consecutive values that do not overlap")
-    return t.data_ptr(), max(t.stride(0), D)
+    return t.data_ptr(), pitch if pitch > D else D
 
 
-def _launch(fn, where, args, device, stream):
+def _launch(torch, fn, where, args, device, stream):
     """Calls a C entry point on `stream` (default: the current stream of the tensors' device) with that device current."""
-    torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif not isinstance(stream, int) and stream.device != device:
+        # the handle alone: a torch Stream object costs as much as the rest of a small call's checks
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        handle = raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
+    elif isinstance(stream, int):
+        handle = stream
+    elif stream.device != device:
         raise ValueError(f"stream is on {stream.device}, expected {device}")
-    handle = stream if isinstance(stream, int) else stream.cuda_stream
-    if device.index == torch.cuda.current_device():
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
         st = fn(ctypes.byref(args), handle)
     else:
         with torch.cuda.device(device):
@@ -598,12 +603,12 @@ def qlinear_block_norm(residual, M, D, *, y=None, residual_scale=1.0, post_norm=
     a = ql_block_norm_args()
     a.M, a.D, a.residual_scale = M, D, residual_scale
     a.residual = _operand(residual, "residual", stream_types, shape, dev)
-    a.residual_dtype = _value_dtype(residual, "residual")
+    a.residual_dtype = _value_dtype(torch, residual, "residual")
     if dev.type != "cuda":
         raise ValueError("residual must be a device tensor")
     if y is not None:
         a.y = _operand(y, "y", stream_types, shape, dev)
-        a.y_dtype = _value_dtype(y, "y")
+        a.y_dtype = _value_dtype(torch, y, "y")
     a.post_norm, a.post_eps, a.pre_norm, a.pre_eps = post_norm, post_eps, pre_norm, pre_eps
     if post_weight is not None:
         a.post_weight = _operand(post_weight, "post_weight", f32, (D,), dev)
@@ -625,11 +630,11 @@ def qlinear_block_norm(residual, M, D, *, y=None, residual_scale=1.0, post_norm=
         a.mod_rows = mod_rows
         need = -(-M // mod_rows) if mod_rows > 0 else 1
     if gate is not None:
-        a.gate, a.gate_ld = _modulation(gate, "gate", need, D, dev)
+        a.gate, a.gate_ld = _modulation(torch, gate, "gate", need, D, dev)
     if scale is not None:
-        a.scale, a.scale_ld = _modulation(scale, "scale", need, D, dev)
+        a.scale, a.scale_ld = _modulation(torch, scale, "scale", need, D, dev)
     if shift is not None:
-        a.shift, a.shift_ld = _modulation(shift, "shift", need, D, dev)
+        a.shift, a.shift_ld = _modulation(torch, shift, "shift", need, D, dev)
     if residual_out is not None:
         a.residual_out = _operand(residual_out, "residual_out", (residual.dtype,), shape, dev)
     if h is not None:
@@ -638,7 +643,7 @@ def qlinear_block_norm(residual, M, D, *, y=None, residual_scale=1.0, post_norm=
         a.x16 = _operand(x16, "x16", (torch.float16,), shape, dev)
     if rowscale is not None:
         a.rowscale = _operand(rowscale, "rowscale", f32, (M,), dev)
-    _launch(lib.qlinear_block_norm, "qlinear_block_norm", a, dev, stream)
+    _launch(torch, lib.qlinear_block_norm, "qlinear_block_norm", a, dev, stream)
 
 
 def qlinear_adapters_workspace_bytes(M, N, K, rank, adapters) -> int:
@@ -680,8 +685,8 @@ def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, 
         f.scaling = _operand(scaling, "scaling", (torch.float32,), (n,), dev)
     if y is not None:
         f.y = _operand(y, "y", (torch.float32, torch.bfloat16), (M, N), dev)
-        f.y_dtype = _value_dtype(y, "y")
-    f.out_dtype = _value_dtype(out, "out")
+        f.y_dtype = _value_dtype(torch, y, "y")
+    f.out_dtype = _value_dtype(torch, out, "out")
     f.out = _operand(out, "out", (out.dtype,), (M, N // 2 if epilogue == QL_EPI_SWIGLU else N), dev)
     f.epilogue = epilogue
     if epilogue == QL_EPI_GATE_RESIDUAL:
@@ -705,7 +710,7 @@ def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, 
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         f.workspace = workspace.data_ptr()
         f.workspace_bytes = workspace.numel() * workspace.element_size()
-    _launch(lib.qlinear_adapters, "qlinear_adapters", f, dev, stream)
+    _launch(torch, lib.qlinear_adapters, "qlinear_adapters", f, dev, stream)
     return out
 
 
