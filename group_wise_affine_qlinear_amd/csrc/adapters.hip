@@ -20,6 +20,7 @@
 // sum of two bf16 terms), v is fp32 and enters the second product as three
 // bf16 terms (24 bits), accumulation is fp32, the output is rounded once.
 #include <algorithm>
+#include <type_traits>
 
 #include "ql_block.h"
 #include "ql_kernels.h"
@@ -248,14 +249,17 @@ __device__ __forceinline__ void unpack4(const Raw4<T, VEC> &r, float (&f)[4]) {
   }
 }
 
-// Columns n .. n + 3 of rows of `width` values, `pitch` apart. A column past
-// the width, or a row that is not live, has its offset past the buffer's end:
-// its loads give zero and its stores are dropped.
+// A lane's four columns of rows of `width` values, `pitch` apart: n .. n + 3,
+// or one by one n, n + 16, n + 32, n + 48, so that neighbouring lanes have
+// neighbouring columns either way. A column past the width, or a row that is
+// not live, has its offset past the buffer's end: its loads give zero and its
+// stores are dropped.
 template <bool VEC> struct Tile {
   int n, width, pitch;
   static constexpr int kPast = 0x7FFFFFF0;
   __device__ __forceinline__ int at(int row, int first, int s, bool live, int size) const {
-    return live && n + s < width ? (row * pitch + first + n + s) * size : kPast;
+    const int c = n + (VEC ? s : 16 * s);
+    return live && c < width ? (row * pitch + first + c) * size : kPast;
   }
   template <typename T>
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int row, int first, bool live, Raw4<T, VEC> &raw) const {
@@ -300,7 +304,8 @@ template <bool VEC> struct Tile {
 // (fp32, zero past the adapter's rank), so that they are read once per block
 // and not once per 64 columns. Subtile s of a wave covers columns 4*c + s: a
 // lane ends with four consecutive columns of four rows, and 16 lanes load and
-// store a contiguous 256 (fp32) or 128 bytes of a row. SwiGLU has the same
+// store a contiguous 256 (fp32) or 128 bytes of a row. Rows that do not start
+// on four elements have c + 16*s instead, a column to an access. SwiGLU has the same
 // columns twice, from the gate and the up half. KB steps of 32 ranks of B
 // stay in registers over the rows (0: any rank, B read again for every 16 rows).
 //
@@ -330,7 +335,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
     const uint16_t *const b = a.b + (int64_t)cur * a.N * a.rank;
 
     // B of the wave's 64 columns from n0 of half h, ranks k0 .. k0 + 31: rows
-    // (columns of out) 4 r16 + s, ranks 8 g .. 8 g + 7 of subtile s. With TURN,
+    // (columns of out) 4 r16 + s, or r16 + 16 s, ranks 8 g .. 8 g + 7 of subtile s. With TURN,
     // where it is read for every step, it is loaded four neighbouring lanes to
     // a row's 64 bytes and turned in LDS of the wave's own: in operand order
     // neighbouring lanes are 4 rows apart, and such loads run at a quarter of
@@ -343,7 +348,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         raw[q] = u32x4{0, 0, 0, 0};
-        const int row = TURN ? q * 16 + (lane >> 2) : 4 * r16 + q;
+        const int row = TURN ? q * 16 + (lane >> 2) : VEC ? 4 * r16 + q : 16 * q + r16;
         const int64_t col = min(n0 + row, width - 1) + (int64_t)h * width;
         if (k < rank) raw[q] = *reinterpret_cast<const u32x4 *>(b + col * a.rank + k);
       }
@@ -351,7 +356,8 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
     auto turn = [&](u32x4 (&raw)[4]) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int row = q * 4 + (lane >> 4), s = (lane >> 2) & 3;
+        // of column 16 q + lane / 4: its lane r16 and subtile s
+        const int row = VEC ? q * 4 + (lane >> 4) : lane >> 2, s = VEC ? (lane >> 2) & 3 : q;
         stage[(s * 16 + row) * 4 + ((lane & 3) ^ (row & 3))] = raw[q];
       }
 #pragma unroll
@@ -374,7 +380,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
     Raw4<F32, VEC> gate_raw;
     u32x4 b_raw[HALVES][KB ? KB : 1][4];
     auto wave_column = [&](int ch) { return (first + ch) * (64 * kWaves) + wave * 64; };
-    auto column = [&](int ch) { return wave_column(ch) + 4 * r16; };
+    auto column = [&](int ch) { return wave_column(ch) + (VEC ? 4 * r16 : r16); };
     auto live = [&](int i, int e) -> bool { return (rows >> (16 * i + 4 * g + e)) & 1; };
     auto load_streams = [&](int ch, int i) {
       const int64_t m = m0 + 16 * i;
@@ -578,11 +584,20 @@ void launch_up(const AdapterArgs &a, const AdapterPlan &p, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, grid, block, lds, stream, a, p.slots, p.splits, col_blocks, chunks, skip);
   };
   constexpr unsigned turn = kWaves * 4096;
-  if (!a.vec) run(adapter_up_kernel<MI, 0, F16, YT, OT, EPI, false>, turn);
-  else if (a.rank <= 32) run(adapter_up_kernel<MI, 1, F16, YT, OT, EPI, true>, 0);
-  else if (a.rank <= 64) run(adapter_up_kernel<MI, 2, F16, YT, OT, EPI, true>, 0);
-  else if (EPI != 1 && a.rank <= 128) run(adapter_up_kernel<MI, EPI != 1 ? 4 : 0, F16, YT, OT, EPI, true>, 0);
-  else run(adapter_up_kernel<MI, 0, F16, YT, OT, EPI, true>, turn);
+  const auto by_rank = [&](auto vec) {
+    constexpr bool VEC = decltype(vec)::value;
+    if (a.rank <= 32) return run(adapter_up_kernel<MI, 1, F16, YT, OT, EPI, VEC>, 0);
+    if (a.rank <= 64) return run(adapter_up_kernel<MI, 2, F16, YT, OT, EPI, VEC>, 0);
+    // beyond 64 ranks B stays in registers for the four steps of a 64-row tile
+    // only (600 x 256 -> 17367 at rank 96, 16-row tiles: 67 us kept, 56 read by
+    // steps); with SwiGLU twice the table's rows do not fit
+    if constexpr (MI == 4 && EPI != 1) {
+      if (a.rank <= 128) return run(adapter_up_kernel<MI, 4, F16, YT, OT, EPI, VEC>, 0);
+    }
+    run(adapter_up_kernel<MI, 0, F16, YT, OT, EPI, VEC>, turn);
+  };
+  if (a.vec) by_rank(std::true_type{});
+  else by_rank(std::false_type{});
 }
 
 template <int MI, bool F16, typename YT, typename OT>
@@ -617,10 +632,12 @@ hipError_t launch_mi(const AdapterArgs &a, const AdapterPlan &p, hipStream_t str
 
 AdapterPlan adapter_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t adapters) {
   AdapterPlan p{};
-  // 16-row tiles up to 1024 rows: more blocks, and fewer adapters to a tile of
-  // short requests (512 rows of 16 requests, 4608 -> 4608 at rank 16: 16.3 us,
-  // with 64-row tiles 20.4; 1024 rows of 8 at rank 32: 21.8 and 24.5)
-  p.row_tile = M <= 1024 ? 16 : 64;
+  // 64-row tiles from 1024 blocks of the second launch and more than 1024 rows,
+  // 16-row tiles below: more blocks, and fewer adapters to a tile of short
+  // requests (512 rows of 16 requests, 4608 -> 4608 at rank 16: 16.3 us, with
+  // 64-row tiles 20.4; 1186 rows of 28, 320 -> 1173 at rank 8: 16.0 and 28.9)
+  const int64_t col_blocks = (N + 64 * kWaves - 1) / (64 * kWaves);
+  p.row_tile = M > 1024 && M / 64 * col_blocks >= 1024 ? 64 : 16;
   p.tiles = (M + p.row_tile - 1) / p.row_tile;
   // Few tiles: blocks of their own for the adapters of one tile, 128 over all
   // tiles (203 rows of 14 requests: 11.1 us, at 32 over all 16.5; 256 rows of
@@ -629,7 +646,6 @@ AdapterPlan adapter_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t adap
   p.slots = (int)std::min<int64_t>(distinct, std::max<int64_t>(1, (p.row_tile == 16 ? 128 : 1) / p.tiles));
   // columns of a block of the second launch: 512 where 256 leave plenty of
   // blocks, so that v is summed less often (SwiGLU case 105 -> 96 us)
-  const int64_t col_blocks = (N + 64 * kWaves - 1) / (64 * kWaves);
   p.chunks = p.tiles * p.slots * col_blocks >= 2048 ? 2 : 1;
   // K ranges of the first launch, by its time and the second's: about 1 us for
   // each 64-wide unit of a wave and 2 us to start, in as many rounds as the
