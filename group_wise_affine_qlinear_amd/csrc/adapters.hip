@@ -81,6 +81,14 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// Between a wave's writes to its own part of LDS and its reads of what other
+// lanes wrote: LDS serves a wave's accesses in order, so only the compiler has
+// to keep them there.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // The adapter of each of a tile's T rows, one lane per row: an index of the
 // table, -1 for a row without one (any index outside the table), -2 past M.
 template <int T>
@@ -179,6 +187,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_down_kernel(AdapterArgs a
       for (int u = u0 + wk; u < u1; u += KW) {
 #pragma unroll
         for (int i = 0; i < 2 * (MI + RJ); ++i) stage[i * 64 + put] = line[i];
+        wave_lds_fence();
         load(min(u + KW, u1 - 1));
         __builtin_amdgcn_sched_barrier(0);  // requested before the products
 #pragma unroll
@@ -196,6 +205,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_down_kernel(AdapterArgs a
               for (int k = 0; k < NT; ++k) acc[i][j] = mfma(w[k], x[i], acc[i][j]);
           }
         }
+        wave_lds_fence();
       }
     }
     __syncthreads();  // every wave's operands, and the previous adapter's sums, have been read
@@ -360,8 +370,10 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
         const int row = VEC ? q * 4 + (lane >> 4) : lane >> 2, s = VEC ? (lane >> 2) & 3 : q;
         stage[(s * 16 + row) * 4 + ((lane & 3) ^ (row & 3))] = raw[q];
       }
+      wave_lds_fence();
 #pragma unroll
       for (int s = 0; s < 4; ++s) raw[s] = stage[(s * 16 + r16) * 4 + (g ^ (r16 & 3))];
+      wave_lds_fence();
     };
     auto mask_b = [&](int k0, u32x4 &raw) {
       if (k0 + 32 <= rank) return;

@@ -1023,7 +1023,7 @@ QL_API int qlinear_adapters(const ql_adapter_args *a, void *stream) {
   k.epilogue = a->epilogue;
   k.residual = gated ? a->residual : nullptr;
   k.gate = gated ? a->gate : nullptr;
-  k.gate_rows = gated ? a->gate_rows : 1;
+  k.gate_rows = gated ? std::min(a->gate_rows, a->M) : 1;  // rows and quotients in 32 bits on the device
   k.v = static_cast<float *>(a->workspace);
   k.vec = width % 4 == 0 && aligned16(a->out) && aligned16(a->y) && aligned16(k.residual) && aligned16(k.gate);
   char buf[160];

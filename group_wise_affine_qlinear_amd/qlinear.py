@@ -704,7 +704,11 @@ def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, 
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             if stream is not None:
                 # taken on the current stream: kept from reuse until the call's stream is done with it
-                workspace.record_stream(torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream)
+                if isinstance(stream, int):
+                    workspace.record_stream(torch.cuda.ExternalStream(stream, device=dev) if stream
+                                            else torch.cuda.default_stream(dev))
+                else:
+                    workspace.record_stream(stream)
     if workspace is not None:
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")

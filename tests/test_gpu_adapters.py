@@ -126,7 +126,7 @@ SIZES = [
     (16, 256, 320, 32, 20), (17, 257, 512, 40, 5), (63, 255, 64, 64, 7), (64, 512, 640, 72, 64), (65, 1003, 448, 128, 3),
     (130, 64, 1024, 256, 9), (255, 36, 2048, 16, 1), (256, 260, 128, 8, 40), (257, 300, 576, 16, 6), (300, 1001, 64, 48, 2),
     (321, 130, 4608, 136, 5), (640, 512, 832, 64, 11), (1000, 96, 256, 32, 3), (33, 8, 12288, 16, 2),
-    # more than 1024 rows: 64-row tiles
+    # more than 1024 rows of few columns
     (1025, 64, 64, 8, 1), (1030, 260, 192, 64, 5), (1100, 67, 320, 136, 9), (1500, 128, 128, 16, 70), (1091, 512, 704, 24, 3),
     (2100, 36, 1024, 256, 2), (1200, 300, 2048, 48, 4), (1063, 1000, 320, 32, 12),
 ]
@@ -139,6 +139,80 @@ def test_sizes(torch, M, N, K, rank, n, ids):
     p = Problem(torch, M, N, K, rank, n, ids=ids, y=["f32", "bf16"][i % 2], out=["f32", "f32", "bf16"][i % 3],
                 table=["bf16", "f16"][(i // 2) % 2], scaling=i % 4 != 3)
     p.check(p.call())
+
+
+LARGE = [
+    # 64-row tiles (more than 1024 rows, many columns), every rank class, whole and odd widths
+    (1030, 16132, 128, 16, 3, "sorted", "none"), (1100, 15617, 192, 24, 2, "sorted", "none"),
+    (1100, 15620, 320, 64, 3, "mixed", "gate"), (1090, 15700, 64, 136, 70, "mixed", "none"),
+    (2048, 8200, 128, 256, 2, "sorted", "gate"), (1100, 16390, 64, 128, 4, "sorted", "swiglu"),
+    (1031, 16404, 704, 8, 5, "mixed", "swiglu"), (1100, 15617, 64, 104, 2, "sorted", "none"),
+    (1100, 15750, 64, 48, 2, "sorted", "swiglu"),
+]
+
+
+@pytest.mark.parametrize("table", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K,rank,n,ids,epilogue", LARGE)
+def test_large_tiles(torch, M, N, K, rank, n, ids, epilogue, table):
+    i = LARGE.index((M, N, K, rank, n, ids, epilogue))
+    ranks = [max(1, rank - 3 * j) for j in range(n)] if i % 2 else None
+    p = Problem(torch, M, N, K, rank, n, ids=ids, y=["f32", "bf16"][i % 2], out=["f32", "bf16", "bf16"][i % 3],
+                table=table, epilogue=epilogue, ranks=ranks)
+    out = p.call()
+    assert "rows64" in ql.qlinear_last_path()
+    p.check(out)
+    if table == "bf16":
+        # rows in another order: the same bits at their new places
+        perm = torch.randperm(M, generator=torch.Generator().manual_seed(i)).cuda()
+        if epilogue != "gate":
+            again = p.call(x=p.x[perm].contiguous(), ids=p.ids[perm].contiguous(), y=p.y[perm].contiguous())
+            assert torch.equal(again, out[perm])
+        # what others hold
+        mine = (p.ids >= 0) & (p.ids < n) & (p.ids != 1)
+        q = {k: getattr(p, k).clone() for k in ("x", "a", "b", "y")}
+        q["x"][~mine] = float("nan")
+        q["a"][1] = float("inf")
+        q["b"][1] = float("nan")
+        assert torch.equal(p.call(**q)[mine], out[mine])
+
+
+def test_large_tiles_in_a_graph(torch):
+    """The largest LDS request (rank 256) and 64-row tiles, captured."""
+    p = Problem(torch, 2048, 8200, 128, 256, 2, ids="sorted")
+    want = p.call()
+    out = torch.empty_like(want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        p.call(out)
+    for _ in range(4):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        eager = p.call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(eager, want)
+
+
+def test_one_gate_row_for_all(torch):
+    """gate_rows beyond M, also beyond 32 bits: one row of the gate."""
+    p = Problem(torch, 40, 260, 128, 16, 3, epilogue="gate")
+    p.gate = p.gate[:1].contiguous()
+    p.gate_rows = 40
+    want = p.call()
+    p.check(want)
+    for rows in (41, 2 ** 32, 2 ** 33 + 5, 2 ** 62):
+        assert torch.equal(p.call(gate_rows=rows), want)
+
+
+def test_gate_rows_of_every_size(torch):
+    """Samples that begin anywhere among the 16 rows of a step."""
+    for rows in (1, 3, 7, 15, 16, 17, 33):
+        p = Problem(torch, 50, 132, 64, 8, 2, epilogue="gate", seed=rows)
+        p.gate_rows = rows
+        p.gate = torch.tanh(torch.randn(-(-50 // rows), 132, generator=torch.Generator().manual_seed(rows))).cuda()
+        p.check(p.call())
 
 
 @pytest.mark.parametrize("epilogue", ["none", "swiglu", "gate"])
@@ -345,6 +419,8 @@ def test_two_streams(torch):
         for p, s, o in zip(ps, streams, outs):
             p.call(o, stream=s)
             p.call(o, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    ps[0].call(outs[0], stream=0)
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
