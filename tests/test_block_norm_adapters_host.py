@@ -205,3 +205,34 @@ def test_adapter_mfma_operands_have_two_wait_states(tmp_path):
     assert res.returncode == 0, res.stderr[-2000:]
     n, bad = scan(out.read_text())
     assert n > 0 and not bad, bad[:5]
+
+
+def test_host_code_under_asan_and_ubsan(tmp_path):
+    """The validation and sizing code of both entry points under the sanitizers (host side only; no call
+    reaches a device): host.cpp as in test_host_asan, with a driver of its own."""
+    import os
+    import shutil
+    import subprocess
+
+    from test_host_asan import HERE, SAN, _run
+
+    from group_wise_affine_qlinear_amd import build as qb
+    others = [os.path.join(qb.BUILD_DIR, os.path.splitext(s)[0] + ".o") for s in qb.SOURCES if s != "host.cpp"]
+    gxx = shutil.which("g++")
+    if not gxx or not all(os.path.exists(o) for o in others):
+        pytest.skip("library objects or g++ missing: run the library build first")
+    host_san = []
+    for f in SAN:
+        host_san += ["-Xarch_host", f]
+    flags = [f for f in qb.COMMON_FLAGS if f != "-O3"]
+    host_obj, drv_obj, exe = (str(tmp_path / n) for n in ("host.o", "driver.o", "driver"))
+    _run([qb.hipcc(), "-x", "hip", *flags, "-O1", "-g", *host_san, "-c", os.path.join(qb.CSRC, "host.cpp"), "-o", host_obj])
+    _run([gxx, "-std=c++17", "-O1", "-g", *SAN, "-I", os.path.join(qb.ROOT, "include"), "-c",
+          os.path.join(HERE, "host_asan", "driver_block.cpp"), "-o", drv_obj])
+    _run([gxx, *SAN, drv_obj, host_obj, *others, "-L", "/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,/opt/rocm/lib", "-o", exe])
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=0:halt_on_error=1", UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1",
+               HIP_VISIBLE_DEVICES="")
+    res = subprocess.run([exe], capture_output=True, text=True, env=env, timeout=300)
+    report = res.stdout + res.stderr
+    assert "AddressSanitizer" not in report and "runtime error" not in report, report
+    assert res.returncode == 0 and "host checks passed" in res.stdout, report

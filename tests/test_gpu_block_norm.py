@@ -56,27 +56,21 @@ def reference(p):
     """r, h in 64 bits with the bounds of their fp32 errors (before the outputs' own rounding)."""
     f = {k: None if p.get(k) is None else np.asarray(p[k], dtype=np.float64) for k in
          ("residual", "y", "post_weight", "post_bias", "pre_weight", "pre_bias", "gate", "scale", "shift")}
-    r = f["residual"] * p["residual_scale"]
+    r = f["residual"] * np.float64(np.float32(p["residual_scale"]))
     e = 2 * U * np.abs(r)
+    one = lambda t, other: np.float64(other) if t is None else t  # noqa: E731
     if f["y"] is not None:
-        z, ez = norm_and_bound(f["y"], np.zeros_like(f["y"]), p["post"], p["post_eps"])
-        for name, step in (("post_weight", "mul"), ("post_bias", "add"), ("gate", "mul")):
-            w = f[name]
-            if w is None:
-                continue
-            z, ez = (z * w, ez * np.abs(w)) if step == "mul" else (z + w, ez)
-            ez = ez + U * np.abs(z)
+        n, en = norm_and_bound(f["y"], np.zeros_like(f["y"]), p["post"], p["post_eps"])
+        gate, bias = one(f["gate"], 1.0), one(f["post_bias"], 0.0)
+        mul, add = one(f["post_weight"], 1.0) * gate, bias * gate
+        z = n * mul + add
         r = r + z
-        e = e + ez + U * np.abs(r)
-    h, eh = norm_and_bound(r, e, p["pre"], p["pre_eps"])
-    for name, step in (("pre_weight", "mul"), ("pre_bias", "add"), ("scale", "mul1"), ("shift", "add")):
-        w = f[name]
-        if w is None:
-            continue
-        if step == "mul1":
-            w, step = 1.0 + w, "mul"
-        h, eh = (h * w, eh * np.abs(w)) if step == "mul" else (h + w, eh)
-        eh = eh + 2 * U * np.abs(h)
+        e = e + np.abs(mul) * en + U * (2 * np.abs(n * mul) + np.abs(add) + np.abs(z) + np.abs(r))
+    n, en = norm_and_bound(r, e, p["pre"], p["pre_eps"])
+    scale, bias, shift = 1.0 + one(f["scale"], 0.0), one(f["pre_bias"], 0.0), one(f["shift"], 0.0)
+    mul, add = one(f["pre_weight"], 1.0) * scale, bias * scale + shift
+    h = n * mul + add
+    eh = np.abs(mul) * en + U * (3 * np.abs(n * mul) + np.abs(bias * scale) + np.abs(add) + np.abs(h))
     want_r, want_h = oracle.block_norm(
         p["residual"], p.get("y"), residual_scale=p["residual_scale"], post=p["post"], post_eps=p["post_eps"],
         post_weight=f["post_weight"], post_bias=f["post_bias"], gate=f["gate"], pre=p["pre"], pre_eps=p["pre_eps"],
