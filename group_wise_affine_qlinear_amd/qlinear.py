@@ -236,6 +236,18 @@ def _u16(torch):
     return (torch.int16, torch.uint16, torch.float16, torch.bfloat16)
 
 
+def _scratch(torch, nbytes, device, stream):
+    """Scratch of a call on ``stream`` (None: the current one) from torch's caching allocator. Taken under the
+    call's own stream: the allocator orders the users of a block by the stream it was taken on alone, so a block of
+    the current stream may still be in use there when a call on another stream begins to write it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 # ------------------------------------------------------------------ device entry points
 
 def qlinear_forward(x, packed_q, scales, biases, bits, group, M, N, K, out):
@@ -329,11 +341,7 @@ def qlinear_forward_ex(x, packed_q, scales, biases, bits, M, N, K, out, *, group
     if nbytes == -1:
         nbytes = int(lib.qlinear_forward_workspace_bytes(ctypes.byref(a)))
         if nbytes > 0:
-            # allocated on the current stream; a call on another stream marks
-            # the tensor in use there so the allocator does not hand it out early
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-            if stream is not None and not isinstance(stream, int):
-                workspace.record_stream(stream)
+            workspace = _scratch(torch, nbytes, x.device, stream)
     if workspace is not None:
         a.workspace = _dev_ptr(workspace, "workspace", (workspace.dtype,))
         a.workspace_bytes = workspace.numel() * workspace.element_size()
@@ -660,7 +668,7 @@ def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, 
     [M, N] and ``out`` fp32 or bf16 (``out`` may be ``y``). ``epilogue=QL_EPI_SWIGLU`` writes ``out`` [M, N/2]
     = silu(t[:, :N/2]) * t[:, N/2:]; ``epilogue=QL_EPI_GATE_RESIDUAL`` writes ``residual`` +
     ``gate``[m // ``gate_rows``] * t. ``workspace`` is a device tensor of
-    ``qlinear_adapters_workspace_bytes`` bytes, by default one from torch's caching allocator.
+    ``qlinear_adapters_workspace_bytes`` bytes, by default one from torch's caching allocator on the call's stream.
     """
     torch = _torch()
     lib = load_library()
@@ -699,16 +707,7 @@ def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, 
         if workspace != TORCH_WORKSPACE:
             raise ValueError(f"workspace must be a device tensor, None or {TORCH_WORKSPACE!r}")
         nbytes = lib.qlinear_adapters_workspace_bytes(M, N, K, rank, n)
-        workspace = None
-        if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            if stream is not None:
-                # taken on the current stream: kept from reuse until the call's stream is done with it
-                if isinstance(stream, int):
-                    workspace.record_stream(torch.cuda.ExternalStream(stream, device=dev) if stream
-                                            else torch.cuda.default_stream(dev))
-                else:
-                    workspace.record_stream(stream)
+        workspace = _scratch(torch, nbytes, dev, stream) if nbytes else None
     if workspace is not None:
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")

@@ -1,0 +1,82 @@
+"""GPU tests of calls queued on the current stream and on another one with no
+wait between them, each with memory that the binding takes for it: both give
+the bits of a call that ran alone. The inputs are complete before the first
+call, and no call reads what another writes, so that nothing but memory that
+the calls would share could order or mix them.
+"""
+import numpy as np
+import pytest
+
+import oracle
+from group_wise_affine_qlinear_amd import inputs
+from group_wise_affine_qlinear_amd import qlinear as ql
+
+from gpu_helpers import dev, torch_or_skip
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    t = torch_or_skip()
+    ql.load_library()
+    return t
+
+
+def in_turn(torch, calls, outs, want, rounds=8):
+    """calls[i](stream) on the current stream and on a side stream in turn, the side stream as an object and a handle."""
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for r in range(rounds):
+        for o in outs:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        calls[0](None)
+        calls[1](side if r % 2 else side.cuda_stream)
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w), r
+    # the legacy default stream by its handle, behind the side stream's call
+    with torch.cuda.stream(side):
+        calls[0](None)
+        calls[1](0)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+@pytest.mark.parametrize("M,N,K,rank", [(1500, 1024, 1024, 32), (40, 512, 4608, 64)])
+def test_adapters(torch, M, N, K, rank):
+    calls, outs, want = [], [], []
+    for seed in (1, 2):
+        g = torch.Generator().manual_seed(seed)
+        x = torch.randn((M, K), generator=g).to(torch.bfloat16).cuda()
+        a = (torch.randn((4, rank, K), generator=g) / K ** 0.5).to(torch.bfloat16).cuda()
+        b = (torch.randn((4, N, rank), generator=g) / rank ** 0.5).to(torch.bfloat16).cuda()
+        ids = torch.sort(torch.randint(0, 4, (M,), generator=g)).values.to(torch.int32).cuda()
+        out = torch.empty((M, N), device="cuda")
+        call = lambda stream, args=(x, a, b, ids, M, N, K, out): ql.qlinear_adapters(*args, stream=stream)  # noqa: E731
+        call(None)
+        torch.cuda.synchronize()
+        calls.append(call)
+        outs.append(out)
+        want.append(out.clone())
+    in_turn(torch, calls, outs, want)
+
+
+@pytest.mark.parametrize("M,N,K,bits", [(1024, 512, 1024, 4), (12, 512, 4608, 4)])
+def test_forward(torch, M, N, K, bits):
+    calls, outs, want = [], [], []
+    for seed in (1, 2):
+        q, s16, b16 = oracle.quantize_rtn(inputs.weights(N, K, seed), bits)
+        x = dev(torch, inputs.activations_bf16(M, K, seed))
+        p, s, b = dev(torch, oracle.pack(q, bits)), dev(torch, s16), dev(torch, b16)
+        out = torch.empty((M, N), device="cuda")
+        call = lambda stream, args=(x, p, s, b, bits, M, N, K, out): ql.qlinear_forward_ex(*args, stream=stream)  # noqa: E731
+        call(None)
+        torch.cuda.synchronize()
+        assert np.isfinite(out.cpu().numpy()).all()
+        calls.append(call)
+        outs.append(out)
+        want.append(out.clone())
+    in_turn(torch, calls, outs, want)
