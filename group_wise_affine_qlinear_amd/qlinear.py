@@ -236,16 +236,25 @@ def _u16(torch):
     return (torch.int16, torch.uint16, torch.float16, torch.bfloat16)
 
 
-def _scratch(torch, nbytes, device, stream):
-    """Scratch of a call on ``stream`` (None: the current one) from torch's caching allocator. Taken under the
+def _empty(torch, shape, dtype, device, stream):
+    """Memory of a call on ``stream`` (None: the current one) from torch's caching allocator. Taken under the
     call's own stream: the allocator orders the users of a block by the stream it was taken on alone, so a block of
     the current stream may still be in use there when a call on another stream begins to write it."""
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(torch, shape, dtype, device, stream):
+    """Memory of a call on ``stream`` that is returned to the caller, who may go on with it on the current stream:
+    kept from reuse until what is queued there when it is freed has run."""
+    t = _empty(torch, shape, dtype, device, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 # ------------------------------------------------------------------ device entry points
@@ -341,7 +350,7 @@ def qlinear_forward_ex(x, packed_q, scales, biases, bits, M, N, K, out, *, group
     if nbytes == -1:
         nbytes = int(lib.qlinear_forward_workspace_bytes(ctypes.byref(a)))
         if nbytes > 0:
-            workspace = _scratch(torch, nbytes, x.device, stream)
+            workspace = _empty(torch, nbytes, torch.uint8, x.device, stream)
     if workspace is not None:
         a.workspace = _dev_ptr(workspace, "workspace", (workspace.dtype,))
         a.workspace_bytes = workspace.numel() * workspace.element_size()
@@ -360,7 +369,7 @@ def qlinear_group_sums(x, M, K, xsum=None, stream=None):
     lib = load_library()
     ld = qlinear_group_sums_ld(M)
     if xsum is None:
-        xsum = torch.empty((K // 64, ld), dtype=torch.float32, device=x.device)
+        xsum = _result(torch, (K // 64, ld), torch.float32, x.device, stream)
     st = lib.qlinear_group_sums(_dev_ptr(x, "x", _u16(torch), (M, K)), M, K,
                                 _dev_ptr(xsum, "xsum", (torch.float32,)), xsum.shape[1],
                                 _stream_handle(stream))
@@ -373,9 +382,9 @@ def qlinear_fast_activations(x, M, K, x16=None, rowscale=None, stream=None):
     torch = _torch()
     lib = load_library()
     if x16 is None:
-        x16 = torch.empty((M, K), dtype=torch.float16, device=x.device)
+        x16 = _result(torch, (M, K), torch.float16, x.device, stream)
     if rowscale is None:
-        rowscale = torch.empty((M,), dtype=torch.float32, device=x.device)
+        rowscale = _result(torch, (M,), torch.float32, x.device, stream)
     st = lib.qlinear_fast_activations(_dev_ptr(x, "x", _u16(torch), (M, K)), M, K,
                                       _dev_ptr(x16, "x16", (torch.float16, torch.int16), (M, K)),
                                       _dev_ptr(rowscale, "rowscale", (torch.float32,), (M,)),
@@ -389,9 +398,9 @@ def qlinear_fast_activations_adaln(x, scale, scale_rows, M, K, x16=None, rowscal
     torch = _torch()
     lib = load_library()
     if x16 is None:
-        x16 = torch.empty((M, K), dtype=torch.float16, device=x.device)
+        x16 = _result(torch, (M, K), torch.float16, x.device, stream)
     if rowscale is None:
-        rowscale = torch.empty((M,), dtype=torch.float32, device=x.device)
+        rowscale = _result(torch, (M,), torch.float32, x.device, stream)
     samples = -(-M // scale_rows) if scale_rows > 0 else 0
     st = lib.qlinear_fast_activations_adaln(_dev_ptr(x, "x", _u16(torch), (M, K)),
                                             _dev_ptr(scale, "scale", (torch.float32,), (samples, K)),
@@ -418,9 +427,9 @@ def qlinear_repack(packed_q, scales, biases, bits, group, N, K, tiled_q=None, ti
     lib = load_library()
     dev = packed_q.device
     if tiled_q is None:
-        tiled_q = torch.empty(qlinear_tiled_words(bits, N, K), dtype=torch.int32, device=dev)
+        tiled_q = _result(torch, (qlinear_tiled_words(bits, N, K),), torch.int32, dev, stream)
     if tiled_sb is None:
-        tiled_sb = torch.empty(qlinear_tiled_sb_words(N, K), dtype=torch.int32, device=dev)
+        tiled_sb = _result(torch, (qlinear_tiled_sb_words(N, K),), torch.int32, dev, stream)
     st = lib.qlinear_repack(
         _dev_ptr(packed_q, "packed_q", (torch.int32, torch.uint32), (N, K * bits // 32)),
         _dev_ptr(scales, "scales", u16, (N, K // group)),
@@ -439,9 +448,9 @@ def qlinear_repack_glu(packed_q, scales, biases, bits, group, N, K, tiled_q=None
     lib = load_library()
     dev = packed_q.device
     if tiled_q is None:
-        tiled_q = torch.empty(qlinear_tiled_words(bits, N, K), dtype=torch.int32, device=dev)
+        tiled_q = _result(torch, (qlinear_tiled_words(bits, N, K),), torch.int32, dev, stream)
     if tiled_sb is None:
-        tiled_sb = torch.empty(qlinear_tiled_sb_words(N, K), dtype=torch.int32, device=dev)
+        tiled_sb = _result(torch, (qlinear_tiled_sb_words(N, K),), torch.int32, dev, stream)
     st = lib.qlinear_repack_glu(
         _dev_ptr(packed_q, "packed_q", (torch.int32, torch.uint32), (N, K * bits // 32)),
         _dev_ptr(scales, "scales", u16, (N, K // group)),
@@ -707,7 +716,7 @@ def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, 
         if workspace != TORCH_WORKSPACE:
             raise ValueError(f"workspace must be a device tensor, None or {TORCH_WORKSPACE!r}")
         nbytes = lib.qlinear_adapters_workspace_bytes(M, N, K, rank, n)
-        workspace = _scratch(torch, nbytes, dev, stream) if nbytes else None
+        workspace = _empty(torch, nbytes, torch.uint8, dev, stream) if nbytes else None
     if workspace is not None:
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")

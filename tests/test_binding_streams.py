@@ -125,3 +125,27 @@ def test_scratch_is_taken_on_the_stream_of_the_call(taken, call, stream, handle)
 def test_scratch_of_the_caller_is_used(taken, call):
     call(Stream(SIDE), workspace=Tensor((4096,), torch.uint8))
     assert taken == []
+
+
+def _results(name, stream):
+    M, N, K = 8, 64, 128
+    u16 = torch.int16
+    x = Tensor((M, K), u16)
+    if name == "qlinear_group_sums":
+        return [ql.qlinear_group_sums(x, M, K, stream=stream)]
+    if name == "qlinear_fast_activations":
+        return ql.qlinear_fast_activations(x, M, K, stream=stream)
+    if name == "qlinear_fast_activations_adaln":
+        return ql.qlinear_fast_activations_adaln(x, Tensor((1, K), torch.float32), M, M, K, stream=stream)
+    weight = Tensor((N, K // 8), torch.int32), Tensor((N, K // 64), u16), Tensor((N, K // 64), u16)
+    return getattr(ql, name)(*weight, 4, 64, N, K, stream=stream)
+
+
+@pytest.mark.parametrize("name", ["qlinear_group_sums", "qlinear_fast_activations", "qlinear_fast_activations_adaln",
+                                  "qlinear_repack", "qlinear_repack_glu"])
+@pytest.mark.parametrize("stream,handle", STREAMS)
+def test_results_are_taken_on_the_stream_of_the_call(taken, name, stream, handle):
+    """Results also outlive what the current stream does with them."""
+    results = list(_results(name, stream))
+    assert results == taken and all(t.taken_on == handle for t in results)
+    assert all(t.recorded == ([] if stream is None else [CURRENT]) for t in results)

@@ -80,3 +80,27 @@ def test_forward(torch, M, N, K, bits):
         outs.append(out)
         want.append(out.clone())
     in_turn(torch, calls, outs, want)
+
+
+def test_results_of_a_call_on_another_stream(torch):
+    """The FAST activations that a call takes memory for: made on a side stream while the current one still works
+    on a block of the same size that was just freed, then read and freed on the current stream."""
+    M, K = 2048, 4608
+    x = dev(torch, inputs.activations_bf16(M, K, 3))
+    want, want_scale = (t.clone() for t in ql.qlinear_fast_activations(x, M, K))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for r in range(6):
+        busy = torch.zeros((M, K), dtype=torch.float16, device="cuda")
+        for _ in range(4):
+            busy += 1
+        kept = busy.clone()
+        del busy
+        x16, scale = ql.qlinear_fast_activations(x, M, K, stream=side if r % 2 else side.cuda_stream)
+        torch.cuda.current_stream().wait_stream(side)
+        got, got_scale = x16.clone(), scale.clone()
+        del x16, scale
+        ql.qlinear_fast_activations(x * 2, M, K, stream=None)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(got_scale, want_scale), r
+        assert bool((kept == 4).all()), r
