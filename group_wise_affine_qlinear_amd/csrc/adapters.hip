@@ -18,7 +18,11 @@
 //
 // Numerics: x and A enter the bf16 MFMA as they are (fp16 tables as an exact
 // sum of two bf16 terms), v is fp32 and enters the second product as three
-// bf16 terms (24 bits), accumulation is fp32, the output is rounded once.
+// bf16 terms (24 bits), accumulation is fp32, the output is rounded once. A
+// term of a finite value may be zero, and an infinite value has no terms behind
+// the first: where an infinity enters, a sum over terms can be NaN although
+// the sum over the values is infinite. Sums of terms that are not finite are
+// therefore taken again from the values one by one, off the fast path.
 #include <algorithm>
 #include <type_traits>
 
@@ -89,6 +93,22 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// The lane counted anew, of nothing that is at hand: what rarely runs computes
+// its addresses from it, and keeps no register while the fast path runs.
+__device__ __forceinline__ int another_lane() {
+  uint32_t all = ~0u;
+  asm volatile("" : "+v"(all));
+  return __builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0u));
+}
+
+// The kernel's first argument, read anew for the same reason.
+__device__ __forceinline__ AdapterArgs another_args() {
+  typedef __attribute__((address_space(4))) const AdapterArgs *Kernarg;
+  uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  return *(const AdapterArgs *)(Kernarg)at;
+}
+
 // The adapter of each of a tile's T rows, one lane per row: an index of the
 // table, -1 for a row without one (any index outside the table), -2 past M.
 template <int T>
@@ -117,6 +137,27 @@ __device__ __forceinline__ int adapter_rank(const AdapterArgs &a, int id) {
   if (id < 0) return 0;
   if (!a.ranks) return a.rank;
   return min(max(a.ranks[id], 0), a.rank);
+}
+
+// The partial sums of a 16 x 16 piece, rows from `row` of the tile and ranks
+// from r, that the fp16 terms left not finite, taken again over [k0, k1).
+__device__ __forceinline__ void sum_values(const AdapterArgs &a, float *v, int cur, int rank, int64_t m0, uint64_t rows,
+                                           int row, int r, int k0, int k1) {
+  const int lane = another_lane();
+  row += lane & 15;
+  r += (lane >> 4) * 4;
+  if (!((rows >> row) & 1)) return;
+  const uint16_t *const x = a.x + (m0 + row) * a.K;
+#pragma clang loop unroll(disable)
+  for (int e = r; e < min(r + 4, rank); ++e) {
+    float *const sum = v + (m0 + row) * a.rank + e;
+    if (__builtin_isfinite(*sum)) continue;
+    const uint16_t *const w = a.a + ((int64_t)cur * a.rank + e) * a.K;
+    float t = 0.f;
+#pragma clang loop unroll(disable)
+    for (int k = k0; k < k1; ++k) t = __builtin_fmaf(bf16_lo(x[k]), f16_to_f32(w[k]), t);
+    *sum = t;
+  }
 }
 
 // v = A x over a range of K. Block: WR*MI*16 rows, RJ*16 ranks; its waves are
@@ -218,6 +259,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_down_kernel(AdapterArgs a
     __syncthreads();
     if (wk == 0) {
       float *v = a.v + (int64_t)blockIdx.y * a.M * a.rank;
+      uint32_t again = 0;  // pieces with a sum of fp16 terms that is not finite
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const int row = first + i * 16 + r16;
@@ -227,8 +269,14 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_down_kernel(AdapterArgs a
 #pragma unroll
           for (int w = 0; w < KW - 1; ++w) t += lds[((w * WR + wr) * (MI * RJ) + i * RJ + j) * 64 + lane];
           const int r = r0 + j * 16 + g * 4;
+          const float zero = (t[0] * 0.f + t[1] * 0.f) + (t[2] * 0.f + t[3] * 0.f);  // NaN where a sum is not finite
           if (((rows >> row) & 1) && r < a.rank) *reinterpret_cast<f32x4 *>(v + (m0 + row) * a.rank + r) = t;
+          if (F16 && __ballot(!(zero == 0.f)) != 0) again |= 1u << (i * RJ + j);
         }
+      }
+      for (; again != 0; again &= again - 1) {
+        const int piece = __builtin_ctz(again);
+        sum_values(a, v, cur, rank, m0, rows, first + piece / RJ * 16, r0 + piece % RJ * 16, u0 * 64, u1 * 64);
       }
     }
     __syncthreads();  // the sums have been read: the next adapter's operands may take their place
@@ -239,6 +287,15 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_down_kernel(AdapterArgs a
 // +inf for g < -88 and the quotient is then -0.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
+// Clears the ranks from `rank` on of a table's entries k .. k + 7, which may hold anything.
+__device__ __forceinline__ void mask_ranks(int k, int rank, u32x4 &raw) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (k + 2 * e >= rank) raw[e] = 0;
+    else if (k + 2 * e + 1 >= rank) raw[e] &= 0xFFFFu;
+  }
 }
 
 // Sixteen rows from row m of an array [., row_length], as a buffer: at most
@@ -308,6 +365,75 @@ template <bool VEC> struct Tile {
   }
 };
 
+// One step of the second launch, 16 rows from `first` of the tile by 64 columns
+// of out from n0, with sums of terms that are not finite: the same sums, in the
+// place of those that are not finite the sums over the values, and the
+// epilogue, a column at a time. Looking for such sums costs a multiply-add for
+// each of them, 0 to 2 % of a call (QKV 4608 x 4608 -> 13824 rank 32 121.2 and
+// 120.1 us, SwiGLU 4096 x 4608 -> 24576 rank 16 89.3 and 90.4, gated down
+// 16896 x 12288 -> 4608 rank 64 246 and 250), 4 % of SwiGLU at rank 128.
+template <bool F16, typename YT, typename OT, int EPI, bool VEC>
+__device__ __forceinline__ void step_by_values(const f32x4 *vs, int cur, uint64_t rows, int64_t m0, int first, int n0) {
+  constexpr int NT = Terms<F16>::n;
+  constexpr int HALVES = EPI == 1 ? 2 : 1;
+  const AdapterArgs a = another_args();
+  const int lane = another_lane(), r16 = lane & 15, g = lane >> 4;
+  const int64_t width = a.N / HALVES;
+  const int rank = adapter_rank(a, cur), units = (a.rank + 31) / 32 * 8;
+  const uint16_t *const b = a.b + (int64_t)cur * a.N * a.rank;
+#pragma clang loop unroll(disable)
+  for (int s = 0; s < 4; ++s) {
+    const int64_t c = n0 + (VEC ? 4 * r16 + s : 16 * s + r16);
+    f32x4 acc[HALVES];
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) {
+      const uint16_t *const table = b + (min(c, width - 1) + h * width) * a.rank;
+      acc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma clang loop unroll(disable)
+      for (int k0 = 0; k0 < rank; k0 += 32) {
+        const int row = first + r16, u = k0 / 4 + 2 * g;
+        const f32x4 lo = vs[row * units + (u ^ (row & 7))], hi = vs[row * units + ((u + 1) ^ (row & 7))];
+        const float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        bf16x8 vt[3], bt[NT];
+        split3(f, vt);
+        u32x4 w = {0, 0, 0, 0};
+        const int k = k0 + 8 * g;
+        if (k < rank) w = *reinterpret_cast<const u32x4 *>(table + k);
+        mask_ranks(k, rank, w);
+        table_terms<F16>(w, bt);
+#pragma unroll
+        for (int q = 2; q >= 0; --q)
+#pragma unroll
+          for (int p = 0; p < NT; ++p) acc[h] = mfma(vt[q], bt[p], acc[h]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (__builtin_isfinite(acc[h][e])) continue;
+        const int row = first + 4 * g + e;
+        float t = 0.f;
+#pragma clang loop unroll(disable)
+        for (int k = 0; k < rank; ++k)
+          t = __builtin_fmaf(reinterpret_cast<const float *>(vs + row * units + ((k / 4) ^ (row & 7)))[k % 4],
+                             F16 ? f16_to_f32(table[k]) : bf16_lo(table[k]), t);
+        acc[h][e] = t;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = first + 4 * g + e;
+      if (c >= width || !((rows >> row) & 1)) continue;
+      const int64_t m = m0 + row;
+      float t[HALVES];
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) t[h] = (a.y ? YT::load(a.y, m * a.N + h * width + c) : 0.f) + acc[h][e];
+      if constexpr (EPI == 1) t[0] = silu_mul(t[0], t[HALVES - 1]);
+      if constexpr (EPI == 2)
+        t[0] = __builtin_fmaf(a.gate[m / a.gate_rows * width + c], t[0], OT::load(a.residual, m * width + c));
+      OT::store(a.out, m * width + c, t[0]);
+    }
+  }
+}
+
 // out = epilogue(y + scaling * B v). Block: MI*16 rows; its four waves take
 // `chunks` times 256 output columns, 64 each. For one adapter of the tile the
 // block first adds the partial sums of v, scales them and keeps them in LDS
@@ -338,7 +464,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
   const int first = (int)(blockIdx.x % (unsigned)col_blocks) * chunks;
   const int units = (a.rank + 31) / 32 * 8;
   const int id = tile_id<T>(a.row_adapter, m0, a.M, a.adapters, lane);
-  bool again = false;
+  bool later = false;
   each_adapter(id, skip_rows_without ? 0 : -1, blockIdx.y, slots, [&](int cur, uint64_t rows) {
     const int rank = adapter_rank(a, cur);
     const float scaling = cur >= 0 && a.scaling ? a.scaling[cur] : 1.0f;
@@ -376,14 +502,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
       wave_lds_fence();
     };
     auto mask_b = [&](int k0, u32x4 &raw) {
-      if (k0 + 32 <= rank) return;
-      // table entries past the adapter's own rank may hold anything
-      const int k = k0 + g * 8;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (k + 2 * e >= rank) raw[e] = 0;
-        else if (k + 2 * e + 1 >= rank) raw[e] &= 0xFFFFu;
-      }
+      if (k0 + 32 > rank) mask_ranks(k0 + g * 8, rank, raw);
     };
 
     // the streams of rows 16 i .., columns of chunk ch
@@ -431,8 +550,8 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
       load_table(0);
       load_streams(0, i);
     }
-    if (again) __syncthreads();  // the previous adapter's v has been read
-    again = true;
+    if (later) __syncthreads();  // the previous adapter's v has been read
+    later = true;
     for (int u = threadIdx.x; u < T * units; u += 64 * kWaves) {
       const int row = u / units, c = u % units;
       f32x4 t = {0.f, 0.f, 0.f, 0.f};
@@ -452,6 +571,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
     }
     __syncthreads();
     if (!any) return;
+    uint32_t again = 0;  // steps with a sum that is not finite: not stored here, but by step_by_values
     for (;;) {
       f32x4 acc[HALVES][4];
 #pragma unroll
@@ -508,7 +628,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
       const Tile<VEC> out = {column(ch), width, width};
       const uint32_t m32 = (uint32_t)m0 + 16 * i, gate0 = EPI == 2 ? m32 / (uint32_t)a.gate_rows : 0;
       const bool one_gate = EPI != 2 || (m32 + 15) / (uint32_t)a.gate_rows == gate0;
-      float o[4][4];
+      float o[4][4], zero = 0.f;  // zero: NaN where a sum is not finite
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float t[HALVES][4], res[4], gt[4];
@@ -528,12 +648,15 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) zero = __builtin_fmaf(acc[h][s][e], 0.f, zero);
           const float v = t[0][s] + acc[0][s][e];
           if constexpr (EPI == 1) o[e][s] = silu_mul(v, t[HALVES - 1][s] + acc[HALVES - 1][s][e]);
           else if constexpr (EPI == 2) o[e][s] = __builtin_fmaf(gt[s], v, res[s]);
           else o[e][s] = v;
         }
       }
+      const uint32_t this_step = 1u << (ch * MI + i);
       const __amdgpu_buffer_rsrc_t out_buf = tile_buffer(a.out, m0 + 16 * i, width, sizeof(typename OT::type));
       bool keep[4];
 #pragma unroll
@@ -548,10 +671,16 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
       }
       if (more) load_streams(ch, i);
       __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the stores
+      const bool odd = __ballot(zero != 0.f) != 0;
+      if (odd) again |= this_step;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) out.template store<OT>(out_buf, 4 * g + e, keep[e], o[e]);
+      for (int e = 0; e < 4; ++e) out.template store<OT>(out_buf, 4 * g + e, keep[e] && !odd, o[e]);
       __builtin_amdgcn_sched_barrier(0);
       if (!more) break;
+    }
+    for (; again != 0; again &= again - 1) {
+      const int bit = __builtin_ctz(again);
+      step_by_values<F16, YT, OT, EPI, VEC>(vs, cur, rows, m0, bit % MI * 16, wave_column(bit / MI));
     }
   });
 }

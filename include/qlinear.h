@@ -532,7 +532,8 @@ typedef struct ql_adapter_args {
  * their requests run fastest: a tile of consecutive rows is multiplied by
  * each distinct adapter that occurs in it. What other rows, other adapters or
  * table entries past an adapter's own rank hold, infinities and NaN included,
- * never reaches a row. row_adapter, ranks and scaling are read on the device,
+ * never reaches a row; in a row's own values they give what the sums above
+ * give, an infinity or NaN. row_adapter, ranks and scaling are read on the device,
  * so a captured graph serves other requests after they are overwritten.
  * Sums are fp32: x and the tables enter as they are, A x is kept in fp32 (to
  * 24 bits in the second product), out is rounded once. A row's result does

@@ -440,3 +440,58 @@ def test_refused_tensors(torch):
         with pytest.raises((ValueError, TypeError, ql.QLinearError)):
             p.call(**kw)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("table", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,rank,epilogue,out", [
+    (5, 64, 8, "none", "f32"), (40, 67, 40, "none", "bf16"), (40, 132, 72, "gate", "f32"), (41, 131, 48, "gate", "bf16"),
+    (33, 130, 8, "swiglu", "f32"), (34, 264, 48, "swiglu", "f32"), (300, 260, 136, "none", "bf16"),
+    (1100, 16384, 8, "gate", "bf16"), (1100, 16385, 104, "none", "f32"), (1100, 16392, 72, "swiglu", "f32")])
+def test_infinities_give_what_the_definition_gives(torch, table, M, N, rank, epilogue, out):
+    """Infinities and NaN in x, A and B of the row's own adapter: an infinity where the definition's sums are
+    infinite, NaN where they are none. All finite values are small integers, so that every product and sum is exact
+    and has zeros in its lower bits, where a value that is split into terms has zero terms."""
+    K, ranks = 64, [1, 1, 2, rank, 1, 3]
+    n = len(ranks)
+    g = torch.Generator().manual_seed(M + N + rank)
+    whole = lambda lo, hi, *s: torch.randint(lo, hi + 1, s, generator=g).float()  # noqa: E731
+    p = Problem(torch, M, N, K, rank, n, ids="mixed", out=out, epilogue=epilogue, ranks=ranks, table=table)
+    nonzero = lambda t: torch.where(t == 0, torch.ones_like(t), t)  # noqa: E731
+    x, a, b = whole(-3, 3, M, K), nonzero(whole(-2, 2, n, rank, K)), whole(-2, 2, n, N, rank)
+    a[2, 0, 5] = 0.0
+    inf, nan = float("inf"), float("nan")
+    x[0::5, 5], x[1::5, 9], x[1::10, 40] = inf, -inf, inf
+    x[3::20, 7] = nan
+    a[3, rank - 1, 2], a[4, 0, 1], a[4, 0, 60] = -inf, inf, inf
+    b[1, 0::3, 0], b[1, 1::6, 0], b[5, ::4, 1], b[0, ::7, 0] = inf, -inf, inf, nan
+    p.x, p.a, p.b = x.to(torch.bfloat16).cuda(), a.to(p.a.dtype).cuda(), b.to(p.b.dtype).cuda()
+    p.y = whole(-3, 3, M, N).cuda()
+    p.scaling = torch.tensor([1.0, 2.0, 0.5, 1.0, -1.0, 4.0]).cuda()
+    if epilogue == "gate":
+        p.residual, p.gate = whole(-3, 3, M, N).to(p.dtype).cuda(), nonzero(whole(-2, 2, p.gate.shape[0], N)).cuda()
+    got = f64(p.call())
+    x, a, b, s, ids = f64(p.x), f64(p.a), f64(p.b), f64(p.scaling), p.ids.cpu().numpy()
+    cols = np.r_[0:min(N, 400), max(0, N - 400):N] if epilogue == "none" else np.arange(N)
+    with np.errstate(invalid="ignore", over="ignore"):
+        t = f64(p.y)[:, cols]
+        for m in np.flatnonzero((ids >= 0) & (ids < n)):
+            i = ids[m]
+            v = (a[i, :ranks[i]] * x[m]).sum(axis=1)
+            t[m] = t[m] + s[i] * (b[i][cols, :ranks[i]] * v).sum(axis=1)
+        if epilogue == "gate":
+            want = f64(p.residual) + f64(p.gate)[np.arange(M) // p.gate_rows] * t
+        elif epilogue == "swiglu":
+            F = N // 2
+            want = t[:, :F] / (1.0 + np.exp(-t[:, :F])) * t[:, F:]
+        else:
+            got, want = got[:, cols], t
+        # the five rows of the smallest case do not meet every adapter
+        assert M < 30 or (np.isposinf(want).any() and np.isneginf(want).any() and np.isnan(want).any())
+        if epilogue == "swiglu":
+            # silu of a finite value is rounded: the last digits of what is finite, and tiny ones, may differ
+            odd = ~np.isfinite(want)
+            assert np.array_equal(got[odd], want[odd], equal_nan=True)
+            assert np.allclose(got[~odd], want[~odd], rtol=1e-4, atol=1e-30)
+        else:
+            want = f64(torch.from_numpy(want).float().to(p.dtype))  # exact in fp32, rounded once
+            assert np.array_equal(got, want, equal_nan=True)
