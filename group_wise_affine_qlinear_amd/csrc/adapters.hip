@@ -727,13 +727,23 @@ void launch_up(const AdapterArgs &a, const AdapterPlan &p, hipStream_t stream) {
   constexpr unsigned turn = kWaves * 4096;
   const auto by_rank = [&](auto vec) {
     constexpr bool VEC = decltype(vec)::value;
+    // B stays in registers over a block's rows (KB steps of 32 ranks) where that
+    // was measured faster than reading it by steps: up to 64 ranks (4096 x 512
+    // -> 4608 bf16 rank 64: 35 us held, 43 by steps; 500 rows within 7 % either
+    // way), but for SwiGLU of rows by elements, whose two halves then leave one
+    // or two waves per SIMD (2048 x 512 -> 8002 bf16 rank 64: 49 us held, 40 by
+    // steps; 500 rows 26 and 18). From 65 to 128 ranks, 64-row tiles, only
+    // fp32 in and out: the fourth step alone (rank 128 plain: 64 held, 68 by
+    // steps; rank 96, which has three, 62 and 54; bf16 rank 128 60 and 58), and
+    // the gated rows by elements throughout (4096 x 512 -> 4609: rank 96 94 and
+    // 102, rank 128 95 and 114; bf16 109 and 79, 111 and 90).
     if (a.rank <= 32) return run(adapter_up_kernel<MI, 1, F16, YT, OT, EPI, VEC>, 0);
-    if (a.rank <= 64) return run(adapter_up_kernel<MI, 2, F16, YT, OT, EPI, VEC>, 0);
-    // beyond 64 ranks B stays in registers for the four steps of a 64-row tile
-    // only (600 x 256 -> 17367 at rank 96, 16-row tiles: 67 us kept, 56 read by
-    // steps); with SwiGLU twice the table's rows do not fit
-    if constexpr (MI == 4 && EPI != 1) {
-      if (a.rank <= 128) return run(adapter_up_kernel<MI, 4, F16, YT, OT, EPI, VEC>, 0);
+    if constexpr (VEC || EPI != 1) {
+      if (a.rank <= 64) return run(adapter_up_kernel<MI, 2, F16, YT, OT, EPI, VEC>, 0);
+    }
+    if constexpr (MI == 4 && EPI != 1 && std::is_same<YT, F32>::value && std::is_same<OT, F32>::value) {
+      if (a.rank <= 128 && (a.rank > 96 || (EPI == 2 && !VEC)))
+        return run(adapter_up_kernel<MI, 4, F16, YT, OT, EPI, VEC>, 0);
     }
     run(adapter_up_kernel<MI, 0, F16, YT, OT, EPI, VEC>, turn);
   };

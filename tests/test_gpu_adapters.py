@@ -10,6 +10,8 @@ epilogue add one u of what they yield; silu's exponential and reciprocal are
 good to a few u (8 are allowed, times 1 + |g| for the exponential's argument).
 The output's own rounding is half a step (fp32 2^-24, bf16 2^-8, relative).
 """
+import copy
+
 import numpy as np
 import pytest
 
@@ -495,3 +497,33 @@ def test_infinities_give_what_the_definition_gives(torch, table, M, N, rank, epi
         else:
             want = f64(torch.from_numpy(want).float().to(p.dtype))  # exact in fp32, rounded once
             assert np.array_equal(got, want, equal_nan=True)
+
+
+# Widths that end in an odd number of 256-column pieces, the last of them short of two waves' columns.
+PIECES = [("none", 15944), ("none", 15943), ("gate", 15944), ("gate", 15943), ("swiglu", 16528), ("swiglu", 16526)]
+
+
+@pytest.mark.parametrize("rank", [16, 64, 104, 136])
+@pytest.mark.parametrize("epilogue,N", PIECES)
+def test_blocks_of_two_pieces(torch, epilogue, N, rank):
+    """Enough blocks that each takes two 256-column pieces (2048 blocks of one): every epilogue and rank class, rows
+    of whole fours and by elements. Checked at the first columns, at those around the pieces' ends, and at the last."""
+    M, i = 2100, PIECES.index((epilogue, N)) + [16, 64, 104, 136].index(rank)
+    assert -(-M // 64) * -(-N // 256) >= 2048
+    y, out = [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")][i % 4 if rank != 104 else i % 2]
+    n = 4
+    p = Problem(torch, M, N, 128, rank, n, ids=["mixed", "sorted"][i // 2 % 2], y=y, out=out, table=["bf16", "f16"][i // 3 % 2],
+                epilogue=epilogue, ranks=[rank, max(1, rank - 5), 1, rank])
+    got = p.call()
+    assert "rows64" in ql.qlinear_last_path()
+    assert bool(torch.isfinite(got).all())
+    w = p.width
+    ends = [c for e in range(256, w, 256 * 7) for c in range(e - 5, e + 5)]
+    cols = torch.tensor(sorted(set(list(range(0, 200)) + ends + list(range(256 * (w // 256 - 1) - 8, w)))))
+    part = copy.copy(p)
+    both = torch.cat([cols, w + cols]) if epilogue == "swiglu" else cols
+    part.N, part.width = len(both), len(cols)
+    part.b, part.y = p.b[:, both.cuda()], p.y[:, both.cuda()]
+    if epilogue == "gate":
+        part.residual, part.gate = p.residual[:, cols.cuda()], p.gate[:, cols.cuda()]
+    part.check(got[:, cols.cuda()])
