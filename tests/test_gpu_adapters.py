@@ -527,3 +527,35 @@ def test_blocks_of_two_pieces(torch, epilogue, N, rank):
     if epilogue == "gate":
         part.residual, part.gate = p.residual[:, cols.cuda()], p.gate[:, cols.cuda()]
     part.check(got[:, cols.cuda()])
+
+
+@pytest.mark.parametrize("table", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,rank", [(3, 64, 8), (30, 67, 40), (300, 132, 72), (1100, 16000, 16), (1100, 16001, 104)])
+def test_every_bit_of_the_first_product_counts(torch, table, M, N, rank):
+    """Whole numbers whose A x needs up to 24 bits, and tables B that pick one or two of them: every product and
+    sum is exact, so that out has the very bits; a second product that took A x to 16 bits would be off by 2^-9
+    of what it dropped."""
+    K, n = 128, 3
+    g = torch.Generator().manual_seed(N + rank)
+    p = Problem(torch, M, N, K, rank, n, ids="mixed", y=None, table=table)
+    x = torch.randint(128, 256, (M, K), generator=g).float()
+    a = torch.randint(128, 256, (n, rank, K), generator=g).float() * torch.where(
+        torch.rand((n, rank, 1), generator=g) < 0.5, -1.0, 1.0)
+    b = torch.zeros((n, N, rank))
+    pick = torch.randint(0, rank, (n, N, 1), generator=g)
+    b.scatter_(2, pick, 1.0)
+    b.scatter_(2, (pick + 1) % rank, -1.0 * (torch.rand((n, N, 1), generator=g) < 0.5))
+    p.x, p.a, p.b = x.to(torch.bfloat16).cuda(), a.to(p.a.dtype).cuda(), b.to(p.b.dtype).cuda()
+    p.scaling = torch.tensor([1.0, -2.0, 0.5]).cuda()
+    got = f64(p.call())
+    ids = p.ids.cpu().numpy()
+    want = np.zeros((M, N))
+    for i in range(n):
+        rows = np.flatnonzero(ids == i)
+        if not len(rows):
+            continue
+        v = x.double().numpy()[rows] @ a[i].double().numpy().T
+        # exact in fp32, and beyond the 16 bits of two terms
+        assert np.abs(v).max() < 2 ** 23 and (v % 256 != 0).any()
+        want[rows] = float(p.scaling[i]) * (v @ b[i].double().numpy().T)
+    assert np.array_equal(got, want)
