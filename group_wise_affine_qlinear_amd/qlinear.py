@@ -544,7 +544,7 @@ def qlinear_dequantize(packed_q, scales, biases, bits, group, N, K, w_out, strea
 
 def _operand(t, name, dtypes, shape, device):
     """Data pointer of a contiguous tensor of one of the dtypes, of this shape, on this device."""
-    if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
+    if getattr(t, "device", None) == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     _dev_ptr(t, name, dtypes, shape)
     raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -638,10 +638,12 @@ def qlinear_block_norm(residual, M, D, *, y=None, residual_scale=1.0, post_norm=
     if row_sample is not None:
         a.row_sample = _operand(row_sample, "row_sample", (torch.int32,), (M,), dev)
         if samples is None:
-            given = [t.shape[0] for t in (gate, scale, shift) if t is not None]
+            given = [t for t in (gate, scale, shift) if t is not None]
             if not given:
                 raise ValueError("row_sample without gate, scale or shift needs samples")
-            samples = min(given)
+            if not all(isinstance(t, torch.Tensor) and t.dim() == 2 for t in given):
+                raise TypeError(f"gate, scale and shift must be float32 tensors [samples, {D}]")
+            samples = min(t.shape[0] for t in given)
         a.samples = need = samples
     else:
         a.mod_rows = mod_rows
@@ -672,7 +674,8 @@ def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, 
     """C ``qlinear_adapters``: low-rank adapters of many requests beside a projection they share.
 
     ``t[m] = y[m] + scaling[id] * b[id] @ (a[id] @ x[m])`` with ``id = row_adapter[m]`` (int32; outside the
-    table: no adapter), then ``out = t`` or an epilogue of it. ``x`` bf16 [M, K]; ``a`` [adapters, rank, K] and
+    table: no adapter), then ``out = t`` or an epilogue of it. ``x`` bf16 [M, K] (``x`` and ``b`` may be None
+    where nothing of them is read: an empty table, or for ``x`` K = 0); ``a`` [adapters, rank, K] and
     ``b`` [adapters, N, rank], both bf16 or both fp16; ``ranks`` int32 and ``scaling`` fp32 [adapters]; ``y``
     [M, N] and ``out`` fp32 or bf16 (``out`` may be ``y``). ``epilogue=QL_EPI_SWIGLU`` writes ``out`` [M, N/2]
     = silu(t[:, :N/2]) * t[:, N/2:]; ``epilogue=QL_EPI_GATE_RESIDUAL`` writes ``residual`` +
@@ -681,7 +684,10 @@ def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, 
     """
     torch = _torch()
     lib = load_library()
-    if not isinstance(a, torch.Tensor) or a.dim() != 3:
+    for t, name in ((a, "a"), (out, "out")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+    if a.dim() != 3:
         raise ValueError("a must be a tensor [adapters, rank, K]")
     dev = out.device
     if dev.type != "cuda":
@@ -692,9 +698,11 @@ def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, 
     if a.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError("a must be bfloat16 or float16")
     f.ab_dtype = QL_ADAPTER_F16 if a.dtype == torch.float16 else QL_ADAPTER_BF16
-    f.x = _operand(x, "x", (torch.bfloat16, torch.int16, torch.uint16), (M, K), dev)
+    if x is not None or (n > 0 and K > 0):  # not read otherwise
+        f.x = _operand(x, "x", (torch.bfloat16, torch.int16, torch.uint16), (M, K), dev)
     f.a = _operand(a, "a", (a.dtype,), (n, rank, K), dev)
-    f.b = _operand(b, "b", (a.dtype,), (n, N, rank), dev)
+    if b is not None or n > 0:
+        f.b = _operand(b, "b", (a.dtype,), (n, N, rank), dev)
     f.row_adapter = _operand(row_adapter, "row_adapter", (torch.int32,), (M,), dev)
     if ranks is not None:
         f.ranks = _operand(ranks, "ranks", (torch.int32,), (n,), dev)
@@ -718,6 +726,8 @@ def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, 
         nbytes = lib.qlinear_adapters_workspace_bytes(M, N, K, rank, n)
         workspace = _empty(torch, nbytes, torch.uint8, dev, stream) if nbytes else None
     if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError(f"workspace must be a device tensor, None or {TORCH_WORKSPACE!r}")
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         f.workspace = workspace.data_ptr()
