@@ -56,7 +56,8 @@ typedef enum {
   QL_EINVAL = -1,        /* bad size, null pointer, K not a multiple of 64  */
   QL_EALIGN = -2,        /* x / out / packed_q not 16-byte aligned            */
   QL_EUNSUPPORTED = -3,  /* bits not in {2,3,4,8}, group != 64, forced path
-                            that cannot serve the shape                      */
+                            that cannot serve the shape, sizes beyond an
+                            entry point's limits                             */
   QL_EWORKSPACE = -4,    /* caller workspace missing or too small             */
   QL_EHIP = -5,          /* a HIP runtime call or kernel launch failed        */
   QL_ERANGE = -6         /* non-finite weight, or f16 overflow of scale/bias  */
@@ -482,7 +483,7 @@ typedef struct ql_block_norm_args {
  * time; any other length or alignment to the element is served, slower.
  * Returns QL_EINVAL for bad sizes, pitches, norms, eps or missing arrays,
  * QL_EALIGN for a pointer not aligned to its element, QL_EUNSUPPORTED for
- * D > 65536. M == 0 is a no-op. No scratch, no allocation, no synchronization.
+ * D > 65536 or M > 4194303 (2^32 threads of a grid). M == 0 is a no-op. No scratch, no allocation, no synchronization.
  */
 int qlinear_block_norm(const ql_block_norm_args *args, void *stream);
 
@@ -495,7 +496,8 @@ typedef struct ql_adapter_args {
   const void *a;               /* [adapters, rank, K]                           */
   const void *b;               /* [adapters, N, rank]                           */
   int ab_dtype;                /* ql_adapter_dtype of a and b                   */
-  int64_t M, N, K;             /* N as the projection's (2F with QL_EPI_SWIGLU); K a multiple of 64 */
+  int64_t M, N, K;             /* N as the projection's (2F with QL_EPI_SWIGLU); K a multiple of 64;
+                                  M up to 2^31 - 1, N and K up to 2^22          */
   int64_t adapters;            /* adapters in the tables, 0 .. 2^31 - 1         */
   int64_t rank;                /* rows of a, a multiple of 8, 8 .. 256          */
   const int32_t *row_adapter;  /* int32 [M]: adapter of each row; outside
@@ -541,14 +543,16 @@ typedef struct ql_adapter_args {
  * Returns QL_EINVAL for bad sizes, types or missing arrays, QL_EALIGN if x, a,
  * b or the workspace is not 16-byte aligned or another pointer is not aligned
  * to its element, QL_EUNSUPPORTED for a rank that is not a multiple of 8 up to
- * 256 or N or K above 2^22, QL_EWORKSPACE for a missing or too small workspace. M == 0 or N == 0 is
- * a no-op. Calls that share one workspace must not overlap in time; nothing
+ * 256, N or K above 2^22, or more than 2^24 - 1 pieces of 64 rows by 256
+ * columns of out, QL_EWORKSPACE for a missing or too small workspace. x may be
+ * NULL with K == 0 or without adapters, a and b without adapters (and a with
+ * K == 0). M == 0 or N == 0 is a no-op. Calls that share one workspace must not overlap in time; nothing
  * in it is kept from one call to the next. No allocation, no synchronization.
  */
 int qlinear_adapters(const ql_adapter_args *args, void *stream);
 
 /* Bytes of workspace a qlinear_adapters call of these sizes needs (fp32
- * partial sums of A x); 0 for invalid arguments. */
+ * partial sums of A x), with any epilogue; 0 for sizes that no call serves. */
 size_t qlinear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters);
 
 /* Static description of a status code. */
