@@ -590,7 +590,7 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
           for (int s = 0; s < 4; ++s) {
             bf16x8 bt[NT];
             u32x4 w = raw[h][s];
-            mask_b(32 * k, w);
+            if constexpr (KB > 0) mask_b(32 * k, w);
             table_terms<F16>(w, bt);
 #pragma unroll
             for (int q = 2; q >= 0; --q)
@@ -618,6 +618,12 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
           for (int h = 0; h < HALVES; ++h) load_b(wave_column(ch), h, min(32 * k + 32, 32 * (units / 8 - 1)), ahead[h]);
 #pragma unroll
           for (int h = 0; h < HALVES; ++h) turn(now[h]);
+          if (32 * k + 32 > rank) {
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+              for (int s = 0; s < 4; ++s) mask_ranks(32 * k + g * 8, rank, now[h][s]);
+          }
           step(k, now);
 #pragma unroll
           for (int h = 0; h < HALVES; ++h)
@@ -728,22 +734,24 @@ void launch_up(const AdapterArgs &a, const AdapterPlan &p, hipStream_t stream) {
   const auto by_rank = [&](auto vec) {
     constexpr bool VEC = decltype(vec)::value;
     // B stays in registers over a block's rows (KB steps of 32 ranks) where that
-    // was measured faster than reading it by steps: up to 64 ranks (4096 x 512
+    // was measured faster than reading it by steps. Up to 64 ranks (4096 x 512
     // -> 4608 bf16 rank 64: 35 us held, 43 by steps; 500 rows within 7 % either
-    // way), but for SwiGLU of rows by elements, whose two halves then leave one
-    // or two waves per SIMD (2048 x 512 -> 8002 bf16 rank 64: 49 us held, 40 by
-    // steps; 500 rows 26 and 18). From 65 to 128 ranks, 64-row tiles, only
-    // fp32 in and out: the fourth step alone (rank 128 plain: 64 held, 68 by
-    // steps; rank 96, which has three, 62 and 54; bf16 rank 128 60 and 58), and
-    // the gated rows by elements throughout (4096 x 512 -> 4609: rank 96 94 and
-    // 102, rank 128 95 and 114; bf16 109 and 79, 111 and 90).
+    // way), but for SwiGLU of rows by elements, whose two halves leave one or
+    // two waves per SIMD then (2048 x 512 -> 8002 bf16 rank 64: 49 us held, 40
+    // by steps; 500 rows 26 and 18). From 65 to 128 ranks, in 64-row tiles, fp32
+    // in and out but for the gated update of whole fours. In us, held and by
+    // steps, rank 96, 4096 x 4608 -> 4608 and (by elements) 4609: fp32 plain 86
+    // and 88 (92 102), gated 107 and 100; bf16 plain 75 and 67 (80 72), gated 87
+    // and 82 (131 100). Rank 128: bf16 plain 79 and 76 (86 83), gated 91 and 92
+    // (139 117); 4096 x 512, fp32 plain 64 and 68 (68 70), gated 90 and 88 (95
+    // 114).
     if (a.rank <= 32) return run(adapter_up_kernel<MI, 1, F16, YT, OT, EPI, VEC>, 0);
     if constexpr (VEC || EPI != 1) {
       if (a.rank <= 64) return run(adapter_up_kernel<MI, 2, F16, YT, OT, EPI, VEC>, 0);
     }
-    if constexpr (MI == 4 && EPI != 1 && std::is_same<YT, F32>::value && std::is_same<OT, F32>::value) {
-      if (a.rank <= 128 && (a.rank > 96 || (EPI == 2 && !VEC)))
-        return run(adapter_up_kernel<MI, 4, F16, YT, OT, EPI, VEC>, 0);
+    constexpr bool F32S = std::is_same<YT, F32>::value && std::is_same<OT, F32>::value;
+    if constexpr (MI == 4 && F32S && (EPI == 0 || (EPI == 2 && !VEC))) {
+      if (a.rank <= 128) return run(adapter_up_kernel<MI, 4, F16, YT, OT, EPI, VEC>, 0);
     }
     run(adapter_up_kernel<MI, 0, F16, YT, OT, EPI, VEC>, turn);
   };
