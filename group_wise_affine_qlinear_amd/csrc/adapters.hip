@@ -804,7 +804,9 @@ AdapterPlan adapter_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t adap
   const int64_t distinct = std::min<int64_t>({M, (int64_t)p.row_tile, adapters + 1});
   p.slots = (int)std::min<int64_t>(distinct, std::max<int64_t>(1, (p.row_tile == 16 ? 128 : 1) / p.tiles));
   // columns of a block of the second launch: 512 where 256 leave plenty of
-  // blocks, so that v is summed less often (SwiGLU case 105 -> 96 us)
+  // blocks, so that v is summed less often (SwiGLU case 105 -> 96 us). The plan
+  // is that of a call without an epilogue, and so is the workspace's size: with
+  // SwiGLU, out has half of the pieces that are counted here.
   p.chunks = p.tiles * p.slots * col_blocks >= 2048 ? 2 : 1;
   // K ranges of the first launch, by its time and the second's: about 1 us for
   // each 64-wide unit of a wave and 2 us to start, in as many rounds as the
@@ -814,7 +816,7 @@ AdapterPlan adapter_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t adap
   // 46.8 at 8; rank 16, 1 row: 10.3 us at 1, 8.9 at 2, 8.3 at 8.
   const int rj = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
   const int along_k = p.row_tile == 16 || rj == 4 ? kWaves : kWaves / 2;  // waves of a block
-  const int per_cu = p.row_tile == 16 ? (rj == 1 ? 8 : 4) : rj == 1 ? 5 : rj == 2 ? 4 : 2;  // blocks, by their registers
+  const int per_cu = p.row_tile == 16 ? (rj == 1 ? 8 : 4) : rj == 1 ? 5 : rj == 2 ? 4 : 2;  // blocks, by the registers of bf16 tables
   const int64_t blocks = p.tiles * p.slots * ((rank + 16 * rj - 1) / (16 * rj)), held = (int64_t)kCus * per_cu;
   const int64_t units = K / 64;
   const int64_t partial = M * rank * ((col_blocks + p.chunks - 1) / p.chunks + 2) / 4096;

@@ -10,8 +10,13 @@
 //
 // A row is held in registers by W waves, C chunks of 8 values per lane, so
 // every input is read once and every output written once: the kernel is bound
-// by those bytes. Everything is fp32; each output is rounded once, and h is
-// made from the unrounded r.
+// by those bytes. Not so for rows by elements (of a length or alignment that
+// 16-byte accesses cannot serve) above 16384 values: four and eight chunks of a
+// lane do not fit its 128 registers there, since a bf16 value takes one of its
+// own, and up to 200 of them go through scratch memory (512 bf16 rows of 53247
+// before a block 62 us, of 53248 23; between two 235 and 68; 1000 rows of 20001
+// between two 122, of 20000 51). Everything is fp32; each output is rounded
+// once, and h is made from the unrounded r.
 #include <algorithm>
 
 #include "ql_block.h"

@@ -104,3 +104,31 @@ def test_results_of_a_call_on_another_stream(torch):
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(got_scale, want_scale), r
         assert bool((kept == 4).all()), r
+
+
+def test_captured_on_the_stream_that_is_given(torch):
+    """A call that is given the capturing stream, as an object or a handle, takes its scratch from the graph's memory."""
+    M, N, K, rank = 300, 512, 1024, 32
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn((M, K), generator=g).to(torch.bfloat16).cuda()
+    a = (torch.randn((4, rank, K), generator=g) / K ** 0.5).to(torch.bfloat16).cuda()
+    b = (torch.randn((4, N, rank), generator=g) / rank ** 0.5).to(torch.bfloat16).cuda()
+    ids = torch.randint(0, 4, (M,), generator=g).to(torch.int32).cuda()
+    want = ql.qlinear_adapters(x, a, b, ids, M, N, K, torch.empty((M, N), device="cuda"))
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    for stream in (side, side.cuda_stream):
+        side.wait_stream(torch.cuda.current_stream())
+        outs.append(torch.empty((M, N), device="cuda"))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            ql.qlinear_adapters(x, a, b, ids, M, N, K, outs[-1], stream=stream)
+    for r in range(4):
+        for out in outs:
+            out.fill_(float("nan"))
+        eager = ql.qlinear_adapters(x, a, b, ids, M, N, K, torch.empty((M, N), device="cuda"), stream=side)
+        torch.cuda.synchronize()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want) and all(torch.equal(out, want) for out in outs), r
