@@ -905,9 +905,6 @@ bool adapter_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t adapters) {
 }
 bool adapter_rank_ok(int64_t rank) { return rank >= 8 && rank <= kMaxAdapterRank && rank % 8 == 0; }
 
-// Whether the second launch's blocks of 256 columns of out fit a grid.
-bool adapter_grid_ok(const ql::AdapterPlan &p, int64_t width) { return p.tiles * ((width + 255) / 256) * p.slots <= kMaxBlocks; }
-
 size_t adapter_ws(const ql::AdapterPlan &p, int64_t M, int64_t rank, int64_t adapters) {
   return adapters == 0 ? 0 : (size_t)p.splits * (size_t)M * (size_t)rank * 4u;
 }
@@ -979,9 +976,7 @@ QL_API size_t qlinear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, 
   if (!adapter_sizes_ok(M, N, K, adapters) || !adapter_rank_ok(rank) || N > kMaxAdapterColumns || K > kMaxAdapterColumns || M == 0 ||
       N == 0)
     return 0;
-  const ql::AdapterPlan p = ql::adapter_plan(M, N, K, (int)rank, adapters);
-  if (!adapter_grid_ok(p, N % 2 ? N : N / 2)) return 0;  // SwiGLU has half the columns
-  return adapter_ws(p, M, rank, adapters);
+  return adapter_ws(ql::adapter_plan(M, N, K, (int)rank, adapters), M, rank, adapters);
 }
 
 QL_API int qlinear_adapters(const ql_adapter_args *a, void *stream) {
@@ -1005,7 +1000,7 @@ QL_API int qlinear_adapters(const ql_adapter_args *a, void *stream) {
     return QL_EALIGN;
   const ql::AdapterPlan p = ql::adapter_plan(a->M, a->N, a->K, (int)a->rank, a->adapters);
   const int64_t width = glu ? a->N / 2 : a->N;
-  if (!adapter_grid_ok(p, width)) return QL_EUNSUPPORTED;
+  if (p.tiles * ((width + 255) / 256) * p.slots > kMaxBlocks) return QL_EUNSUPPORTED;
   const size_t need = adapter_ws(p, a->M, a->rank, a->adapters);
   if (need > 0 && (!a->workspace || a->workspace_bytes < need)) return QL_EWORKSPACE;
   ql::AdapterArgs k{};

@@ -552,7 +552,9 @@ typedef struct ql_adapter_args {
 int qlinear_adapters(const ql_adapter_args *args, void *stream);
 
 /* Bytes of workspace a qlinear_adapters call of these sizes needs (fp32
- * partial sums of A x), with any epilogue; 0 for sizes that no call serves. */
+ * partial sums of A x); 0 for invalid arguments and for a rank, N or K that
+ * is not supported. Of the number of pieces it knows nothing: it gives a size
+ * for calls that are refused for that alone. */
 size_t qlinear_adapters_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters);
 
 /* Static description of a status code. */

@@ -238,21 +238,18 @@ def test_host_code_under_asan_and_ubsan(tmp_path):
     assert res.returncode == 0 and "host checks passed" in res.stdout, report
 
 
-def test_adapters_workspace_of_calls_that_are_not_served(lib):
-    """Sizes of more blocks than a grid holds with every epilogue need no workspace; at the limit they are served."""
+def test_adapters_piece_limit(lib):
+    """2^24 - 1 pieces of 64 rows by 256 columns of out are served, one more is refused."""
     rows = 64 * ((1 << 24) - 1)
-    for M, N in ((1 << 30, 1 << 20), (rows + 1, 256), (rows + 1, 257), (rows + 1, 255), (rows, 514)):
-        assert ql.qlinear_adapters_workspace_bytes(M, N, 64, 8, 2) == 0, (M, N)
-        for epilogue in (ql.QL_EPI_NONE, ql.QL_EPI_SWIGLU):
-            if epilogue == ql.QL_EPI_SWIGLU and N % 2:
-                continue
-            a = _adapters(M=M, N=N, K=64, rank=8, workspace_bytes=1 << 62, epilogue=epilogue)
-            assert lib.qlinear_adapters(ctypes.byref(a), None) == ql.QL_EUNSUPPORTED, (M, N, epilogue)
-    for M, N, epilogue in ((rows, 256, ql.QL_EPI_NONE), (rows, 512, ql.QL_EPI_SWIGLU)):
+    none, swiglu = ql.QL_EPI_NONE, ql.QL_EPI_SWIGLU
+    for M, N, epilogue, served in ((rows, 256, none, True), (rows, 512, swiglu, True), (rows + 1, 256, none, False),
+                                   (rows + 1, 255, none, False), (rows, 257, none, False), (rows + 1, 512, swiglu, False),
+                                   (rows, 514, swiglu, False), (1 << 30, 1 << 20, none, False)):
         need = ql.qlinear_adapters_workspace_bytes(M, N, 64, 8, 2)
         assert need >= M * 8 * 4
         a = _adapters(M=M, N=N, K=64, rank=8, workspace_bytes=need - 1, epilogue=epilogue)
-        assert lib.qlinear_adapters(ctypes.byref(a), None) == ql.QL_EWORKSPACE
+        want = ql.QL_EWORKSPACE if served else ql.QL_EUNSUPPORTED
+        assert lib.qlinear_adapters(ctypes.byref(a), None) == want, (M, N, epilogue)
 
 
 def test_block_norm_row_limit(lib):
