@@ -559,3 +559,40 @@ def test_every_bit_of_the_first_product_counts(torch, table, M, N, rank):
         assert np.abs(v).max() < 2 ** 23 and (v % 256 != 0).any()
         want[rows] = float(p.scaling[i]) * (v @ b[i].double().numpy().T)
     assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,epilogue", [(90, 260, "none"), (90, 259, "gate"), (1210, 16000, "gate"), (1210, 16001, "none")])
+def test_infinities_in_place_and_in_a_graph(torch, M, N, epilogue, dt):
+    """Steps with infinite sums are stored last, from inputs that the call may be about to overwrite, by arguments that
+    the kernel reads a second time."""
+    p = Problem(torch, M, N, 128, 24, 6, y=dt, out=dt, epilogue=epilogue, ranks=[1, 24, 1, 7, 24, 2])
+    p.x[::7, 3] = float("inf")
+    p.b[2, ::5, 0] = float("-inf")
+    p.a[4, 2, 9] = float("nan")
+    bits = torch.int32 if dt == "f32" else torch.int16
+
+    def same(got, want):  # NaN at the same places, the same bits elsewhere
+        nan = torch.isnan(want)
+        return torch.equal(torch.isnan(got), nan) and torch.equal(got.view(bits)[~nan], want.view(bits)[~nan])
+
+    apart = p.call()
+    assert bool(torch.isinf(apart).any()) and bool(torch.isnan(apart).any())
+    out = p.y.clone()
+    assert same(p.call(out, y=out), apart)
+    if epilogue == "gate":
+        stream = p.residual.clone()
+        assert same(p.call(stream, residual=stream), apart)
+    out = torch.empty_like(apart)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        p.call(out)
+    for _ in range(4):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        eager = p.call()
+        torch.cuda.synchronize()
+        assert same(out, apart) and same(eager, apart)
