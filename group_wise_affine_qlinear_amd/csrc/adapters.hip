@@ -369,9 +369,10 @@ template <bool VEC> struct Tile {
 // of out from n0, with sums of terms that are not finite: the same sums, in the
 // place of those that are not finite the sums over the values, and the
 // epilogue, a column at a time. Looking for such sums costs a multiply-add for
-// each of them, 0 to 2 % of a call (QKV 4608 x 4608 -> 13824 rank 32 121.2 and
-// 120.1 us, SwiGLU 4096 x 4608 -> 24576 rank 16 89.3 and 90.4, gated down
-// 16896 x 12288 -> 4608 rank 64 246 and 250), 4 % of SwiGLU at rank 128.
+// each of them, 0 to 2 % of a call (us before and with it: QKV 4608 x 4608 ->
+// 13824 rank 32 121 and 120, SwiGLU 4096 x 4608 -> 24576 rank 16 89 and 90,
+// gated down 16896 x 12288 -> 4608 rank 64 246 and 249), 2 to 5 % of SwiGLU
+// above rank 64 (2048 x 4608 -> 24576 rank 128 142 and 146).
 template <bool F16, typename YT, typename OT, int EPI, bool VEC>
 __device__ __forceinline__ void step_by_values(const f32x4 *vs, int cur, uint64_t rows, int64_t m0, int first, int n0) {
   constexpr int NT = Terms<F16>::n;
