@@ -101,12 +101,12 @@ __device__ __forceinline__ int another_lane() {
   return __builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0u));
 }
 
-// The kernel's first argument, read anew for the same reason.
-__device__ __forceinline__ AdapterArgs another_args() {
-  typedef __attribute__((address_space(4))) const AdapterArgs *Kernarg;
+// The address of the kernel's first argument, for reading it anew for the same reason.
+typedef __attribute__((address_space(4))) const AdapterArgs *Kernarg;
+__device__ __forceinline__ Kernarg another_args() {
   uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
   asm volatile("" : "+s"(at));
-  return *(const AdapterArgs *)(Kernarg)at;
+  return (Kernarg)at;
 }
 
 // The adapter of each of a tile's T rows, one lane per row: an index of the
@@ -371,13 +371,13 @@ template <bool VEC> struct Tile {
 // epilogue, a column at a time. Looking for such sums costs a multiply-add for
 // each of them, 0 to 2 % of a call (us before and with it: QKV 4608 x 4608 ->
 // 13824 rank 32 121 and 120, SwiGLU 4096 x 4608 -> 24576 rank 16 89 and 90,
-// gated down 16896 x 12288 -> 4608 rank 64 246 and 249), 2 to 5 % of SwiGLU
-// above rank 64 (2048 x 4608 -> 24576 rank 128 142 and 146).
+// gated down 16896 x 12288 -> 4608 rank 64 246 and 249).
 template <bool F16, typename YT, typename OT, int EPI, bool VEC>
-__device__ __forceinline__ void step_by_values(const f32x4 *vs, int cur, uint64_t rows, int64_t m0, int first, int n0) {
+__device__ __forceinline__ void step_by_values(Kernarg args, const f32x4 *vs, int cur, uint64_t rows, int64_t m0, int first,
+                                               int n0) {
   constexpr int NT = Terms<F16>::n;
   constexpr int HALVES = EPI == 1 ? 2 : 1;
-  const AdapterArgs a = another_args();
+  const AdapterArgs a = *(const AdapterArgs *)args;
   const int lane = another_lane(), r16 = lane & 15, g = lane >> 4;
   const int64_t width = a.N / HALVES;
   const int rank = adapter_rank(a, cur), units = (a.rank + 31) / 32 * 8;
@@ -433,6 +433,17 @@ __device__ __forceinline__ void step_by_values(const f32x4 *vs, int cur, uint64_
       OT::store(a.out, m * width + c, t[0]);
     }
   }
+}
+
+// The same as a function of its own, for the kernels that read B by steps: put
+// into the kernel, it slows their loop (SwiGLU 2048 x 4608 -> 24576 rank 72 143
+// us, rank 128 146; called 132 and 139). The others have it inside, where a
+// call takes registers that the loop needs (4096 x 4608 -> 4608 bf16 rank 64
+// four waves per SIMD and 45.3 us, with a call three and 45.9).
+template <bool F16, typename YT, typename OT, int EPI, bool VEC>
+__device__ __attribute__((noinline)) void step_by_values_called(Kernarg args, const f32x4 *vs, int cur, uint64_t rows,
+                                                              int64_t m0, int first, int n0) {
+  step_by_values<F16, YT, OT, EPI, VEC>(args, vs, cur, rows, m0, first, n0);
 }
 
 // out = epilogue(y + scaling * B v). Block: MI*16 rows; its four waves take
@@ -687,7 +698,9 @@ __global__ __launch_bounds__(64 * kWaves) void adapter_up_kernel(AdapterArgs a, 
     }
     for (; again != 0; again &= again - 1) {
       const int bit = __builtin_ctz(again);
-      step_by_values<F16, YT, OT, EPI, VEC>(vs, cur, rows, m0, bit % MI * 16, wave_column(bit / MI));
+      const int first_row = bit % MI * 16, n0 = wave_column(bit / MI);
+      if constexpr (KB == 0) step_by_values_called<F16, YT, OT, EPI, VEC>(another_args(), vs, cur, rows, m0, first_row, n0);
+      else step_by_values<F16, YT, OT, EPI, VEC>(another_args(), vs, cur, rows, m0, first_row, n0);
     }
   });
 }
