@@ -1,0 +1,259 @@
+// From the output of a fused QKV projection to the heads that attention reads
+// (qlinear_qk_norm_rope): per query and key head
+//
+//   u = N(x) * w                               over the D values of the head
+//   t_i = positions[axis_i, m] * freqs[i]      one angle per pair and row
+//   (a, b) -> (a cos t_i - b sin t_i, b cos t_i + a sin t_i)
+//
+// with the pairs (u_i, u_{i + P}) or (u_2i, u_{2i+1}), i < P; values are
+// rounded only. N is the identity, v / sqrt(mean v^2 + eps) or
+// (v - mean) / sqrt(mean (v - mean)^2 + eps).
+//
+// A head lies on the power of two of lanes that holds 8 values each, so a
+// wave works on 64 / lanes heads at once, every value is read once and written
+// once and the sums of a norm are DPP moves. The angles depend on the row
+// alone: a wave makes its lanes' four cosines and sines once per row and turns
+// all of its heads by them.
+#include "ql_block.h"
+#include "ql_kernels.h"
+
+namespace ql {
+
+namespace {
+
+// Sum (or maximum of magnitudes) over the aligned groups of 2^lg lanes, in a
+// fixed order, in every lane of the group.
+template <int CTRL, typename Op>
+__device__ __forceinline__ float dpp(float v, Op op) {
+  return op(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false)));
+}
+template <typename Op>
+__device__ __forceinline__ float group_all(float v, int lg, Op op) {
+  v = dpp<0xB1>(v, op);                // quad_perm [1, 0, 3, 2]
+  v = dpp<0x4E>(v, op);                // quad_perm [2, 3, 0, 1]
+  if (lg > 2) v = dpp<0x141>(v, op);   // row_half_mirror
+  if (lg > 3) v = dpp<0x140>(v, op);   // row_mirror
+  if (lg > 4) {
+    // lane ^ 16: rows 0 <-> 1 and 2 <-> 3
+    const int o = __builtin_amdgcn_ds_swizzle(__builtin_bit_cast(int, v), 0x401F);
+    v = op(v, __builtin_bit_cast(float, o));
+  }
+  return v;
+}
+
+struct Sum {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct Max {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+
+// The 8 values of a lane: four at `lo` and four at `hi` of its head.
+template <typename T, bool VEC>
+struct Piece {
+  u32x4 raw[2];  // bf16: two words of each are used
+
+  __device__ __forceinline__ void load(const void *base, int64_t at, int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t e = at + (i ? hi : lo);
+      if constexpr (__is_same(T, F32)) {
+        const float *p = static_cast<const float *>(base) + e;
+        if constexpr (VEC) raw[i] = *reinterpret_cast<const u32x4 *>(p);
+        else raw[i] = u32x4{__float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]), __float_as_uint(p[3])};
+      } else {
+        const uint16_t *p = static_cast<const uint16_t *>(base) + e;
+        if constexpr (VEC) {
+          const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
+          raw[i][0] = w[0];
+          raw[i][1] = w[1];
+        } else {
+          raw[i][0] = p[0] | (uint32_t)p[1] << 16;
+          raw[i][1] = p[2] | (uint32_t)p[3] << 16;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (__is_same(T, F32)) v[e] = __uint_as_float(raw[e / 4][e % 4]);
+      else v[e] = e % 2 ? bf16_hi(raw[e / 4][e % 4 / 2]) : bf16_lo(raw[e / 4][e % 4 / 2]);
+    }
+  }
+};
+
+template <bool VEC>
+__device__ __forceinline__ void store(uint16_t *base, int64_t at, int lo, int hi, const float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint16_t *p = base + at + (i ? hi : lo);
+    if constexpr (VEC) {
+      *reinterpret_cast<u32x2 *>(p) = u32x2{pack_bf16(v[4 * i], v[4 * i + 1]), pack_bf16(v[4 * i + 2], v[4 * i + 3])};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = bf16_bits(v[4 * i + e]);
+    }
+  }
+}
+
+// N over a head. Lanes past the head hold zeros and `live` false. The mean is
+// taken first and the squares of the centred values second, so a large mean
+// cancels nothing. Where the sums leave fp32 although every value is finite,
+// they are taken again of the values times the power of two that brings the
+// largest into [1, 4); the other heads of the wave go along with a factor of 1.
+__device__ __forceinline__ void normalise(float (&v)[8], int kind, float eps, float inv_d, int lg, bool live) {
+  float unit = 1.f;
+  for (int pass = 0;; ++pass) {
+    float mean = 0.f;
+    if (kind == 2) {
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = __builtin_fmaf(v[e], unit, s);
+      mean = group_all(s, lg, Sum{}) * inv_d;
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float c = __builtin_fmaf(v[e], unit, -mean);
+      if (!live) c = 0.f;
+      q = __builtin_fmaf(c, c, q);
+    }
+    const float var = group_all(q, lg, Sum{}) * inv_d;
+    // the scaled eps may underflow; a variance that is not zero is then far above 2^-126
+    const float rstd = rsqrtf(var + fmaxf(eps * unit * unit, 0x1p-126f));
+    float mx = 0.f;
+    const bool again = pass == 0 && !__builtin_isfinite(var);
+    if (__any(again)) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
+      mx = group_all(mx, lg, Max{});
+      if (again && mx < __builtin_inff()) unit = __uint_as_float((uint32_t)max(254 - (int)(__float_as_uint(mx) >> 23), 1) << 23);
+      continue;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], unit, -mean) * rstd;
+    return;
+  }
+}
+
+// Grid: x rows, y ranges of a row's steps; a step is the 64 >> lg heads that a
+// wave holds at once, the steps of q first, then k's, then v's.
+template <typename T, bool PAIRS, bool VEC>
+__global__ __launch_bounds__(256) void qk_norm_rope_kernel(HeadsArgs a) {
+  const int64_t m = blockIdx.x;
+  if (a.rows_end && m >= *a.rows_end) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lg = a.lane_bits, slot = lane & ((1 << lg) - 1), sub = lane >> lg, per = 64 >> lg;
+  const bool live = slot * 8 < a.D;
+  const int turning = a.pairs / 4;  // slots that hold turned pairs
+  const bool turns = slot < turning;
+  const int lo = !PAIRS && turns ? slot * 4 : slot * 8;
+  const int hi = !PAIRS && turns ? a.pairs + slot * 4 : slot * 8 + 4;
+
+  const int steps_q = (a.part[0].heads + per - 1) / per, steps_k = (a.part[1].heads + per - 1) / per;
+  const int steps = steps_q + steps_k + (a.part[2].heads + per - 1) / per;
+  const int stride = 4 * gridDim.y;
+  // the part, first head and address of step i; the address only where the lane has a head of it
+  auto where = [&](int i, int &p, int64_t &head) {
+    p = i < steps_q ? 0 : i < steps_q + steps_k ? 1 : 2;
+    head = (int64_t)(i - (p == 0 ? 0 : p == 1 ? steps_q : steps_q + steps_k)) * per + sub;
+    return live && i < steps && head < a.part[p].heads;
+  };
+  Piece<T, VEC> next = {};
+  int i = blockIdx.y * 4 + wave;
+  {
+    int p;
+    int64_t head;
+    if (where(i, p, head)) next.load(a.part[p].in, m * a.part[p].in_ld + head * a.D, lo, hi);
+  }
+
+  // angles in turns, in 64 bits: what is left of a far position's angle after
+  // whole turns is then as exact as a near one's
+  float cs[4], sn[4];
+  if (turning > 0 && i < steps_q + steps_k) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      cs[e] = 1.f;
+      sn[e] = 0.f;
+      if (turns) {
+        const int pair = slot * 4 + e;
+        const int axis = a.pair_axis ? a.pair_axis[pair] : 0;
+        if ((unsigned)axis < (unsigned)a.axes) {
+          double t = (double)a.positions[axis * a.M + m] * ((double)a.freqs[pair] * 0.15915494309189533577);
+          t -= rint(t);
+          sincospif(2.f * (float)t, &sn[e], &cs[e]);
+        }
+      }
+    }
+  }
+
+  float w[8];
+  int held = -1;  // part whose weights are in w
+  const float inv_d = 1.f / (float)a.D;
+  for (; i < steps; i += stride) {
+    int p;
+    int64_t head;
+    const bool here = where(i, p, head);
+    float v[8];
+    next.values(v);
+    {
+      int pn;
+      int64_t hn;
+      if (where(i + stride, pn, hn)) next.load(a.part[pn].in, m * a.part[pn].in_ld + hn * a.D, lo, hi);
+    }
+    if (p != 2) {
+      if (!here) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      }
+      if (a.norm) normalise(v, a.norm, a.eps, inv_d, lg, live);
+      if (a.part[p].weight) {
+        if (held != p) {
+          held = p;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = live ? a.part[p].weight[(e < 4 ? lo : hi - 4) + e] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= w[e];
+      }
+      if (turns) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float &x = v[PAIRS ? 2 * e : e], &y = v[PAIRS ? 2 * e + 1 : e + 4];
+          const float x0 = x, y0 = y;
+          x = __builtin_fmaf(x0, cs[e], -(y0 * sn[e]));
+          y = __builtin_fmaf(y0, cs[e], x0 * sn[e]);
+        }
+      }
+    }
+    if (here) store<VEC>(a.part[p].out, m * a.part[p].out_ld + head * a.D, lo, hi, v);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_qk_norm_rope(const HeadsArgs &a, hipStream_t stream) {
+  // Few rows leave CUs idle: their steps are then divided over up to as many
+  // blocks as keep 512 in all, each of which makes the row's angles again.
+  const int per = 64 >> a.lane_bits;
+  int steps = 0;
+  for (const auto &p : a.part) steps += (p.heads + per - 1) / per;
+  const int most = (steps + 3) / 4;
+  const int64_t want = a.M >= 512 ? 1 : 512 / a.M;
+  const dim3 grid((unsigned)a.M, (unsigned)(want < most ? want : most));
+#define QL_HEADS(T, PAIRS, VEC) qk_norm_rope_kernel<T, PAIRS, VEC><<<grid, 256, 0, stream>>>(a)
+#define QL_HEADS_VEC(T, PAIRS) \
+  if (a.vec) QL_HEADS(T, PAIRS, true); \
+  else QL_HEADS(T, PAIRS, false)
+  if (a.in_bf16) {
+    if (a.pair_layout) { QL_HEADS_VEC(BF16, true); } else { QL_HEADS_VEC(BF16, false); }
+  } else {
+    if (a.pair_layout) { QL_HEADS_VEC(F32, true); } else { QL_HEADS_VEC(F32, false); }
+  }
+#undef QL_HEADS_VEC
+#undef QL_HEADS
+  return hipGetLastError();
+}
+
+}  // namespace ql

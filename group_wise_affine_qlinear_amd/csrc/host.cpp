@@ -1031,3 +1031,175 @@ QL_API int qlinear_adapters(const ql_adapter_args *a, void *stream) {
   set_last_path(buf);
   return ql::launch_adapters(k, p, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? QL_OK : QL_EHIP;
 }
+
+namespace {
+
+constexpr int64_t kMaxHeadDim = 256;
+constexpr int64_t kMaxHeads = 65536;
+constexpr int64_t kMaxAttentionRows = int64_t(1) << 30;
+constexpr int64_t kMaxAttentionPitch = int64_t(1) << 22;  // 64 rows of it within a 31-bit offset
+constexpr int64_t kMaxSamples = int64_t(1) << 20;
+
+bool head_dim_ok(int64_t D) { return D >= 8 && D <= kMaxHeadDim && D % 8 == 0; }
+
+}  // namespace
+
+QL_API int qlinear_qk_norm_rope(const ql_qk_args *a, void *stream) {
+  if (!a) return QL_EINVAL;
+  if (a->M < 0 || a->head_dim < 1 || a->q_heads < 0 || a->kv_heads < 0 || a->pairs < 0) return QL_EINVAL;
+  if (!dtype_ok(a->in_dtype) || !norm_ok(a->norm, a->eps)) return QL_EINVAL;
+  if (a->rope != QL_ROPE_HALVES && a->rope != QL_ROPE_PAIRS) return QL_EINVAL;
+  if (!head_dim_ok(a->head_dim) || a->M > kMaxBlocks || a->q_heads > kMaxHeads || a->kv_heads > kMaxHeads ||
+      a->pairs % 4 || a->axes > kMaxHeads)
+    return QL_EUNSUPPORTED;
+  if (a->pairs > a->head_dim / 2) return QL_EINVAL;
+  if ((a->q != nullptr) != (a->q_out != nullptr) || (a->k != nullptr) != (a->k_out != nullptr) ||
+      (a->v != nullptr) != (a->v_out != nullptr))
+    return QL_EINVAL;
+  if ((a->q && a->q_heads < 1) || ((a->k || a->v) && a->kv_heads < 1)) return QL_EINVAL;
+  if ((!a->q && a->q_weight) || (!a->k && a->k_weight)) return QL_EINVAL;
+  if (a->M == 0) return QL_OK;
+  if (!a->q && !a->k && !a->v) return QL_EINVAL;
+  if (a->pairs > 0 && (!a->freqs || !a->positions || a->axes < 1)) return QL_EINVAL;
+  const int64_t D = a->head_dim;
+  const size_t in_bytes = dtype_bytes(a->in_dtype);
+  ql::HeadsArgs k{};
+  const struct {
+    const void *in;
+    void *out;
+    int64_t in_ld, out_ld, heads;
+    const float *weight;
+  } parts[3] = {{a->q, a->q_out, a->q_ld, a->q_out_ld, a->q_heads, a->q_weight},
+                {a->k, a->k_out, a->k_ld, a->k_out_ld, a->kv_heads, a->k_weight},
+                {a->v, a->v_out, a->v_ld, a->v_out_ld, a->kv_heads, nullptr}};
+  bool vec = true;
+  for (int i = 0; i < 3; ++i) {
+    const auto &p = parts[i];
+    if (!p.in) continue;
+    if (p.in_ld < p.heads * D || p.out_ld < p.heads * D) return QL_EINVAL;
+    if (p.in == p.out && (p.in_ld != p.out_ld || a->in_dtype != QL_OUT_BF16)) return QL_EINVAL;
+    vec = vec && on_elements(p.in, 4 * in_bytes) && on_elements(p.out, 8) && p.in_ld % 4 == 0 && p.out_ld % 4 == 0;
+    k.part[i] = {p.in, static_cast<uint16_t *>(p.out), p.in_ld, p.out_ld, p.weight, (int)p.heads};
+  }
+  for (const auto &p : parts)
+    if (!on_elements(p.in, in_bytes) || !on_elements(p.out, 2) || !on_elements(p.weight, 4)) return QL_EALIGN;
+  for (const void *p : {(const void *)a->freqs, (const void *)a->pair_axis, (const void *)a->positions,
+                        (const void *)a->rows_end})
+    if (!on_elements(p, 4)) return QL_EALIGN;
+  k.M = a->M;
+  k.D = (int)D;
+  k.lane_bits = D <= 32 ? 2 : D <= 64 ? 3 : D <= 128 ? 4 : 5;
+  k.in_bf16 = a->in_dtype == QL_OUT_BF16;
+  k.norm = a->norm;
+  k.eps = a->eps;
+  k.pair_layout = a->rope == QL_ROPE_PAIRS;
+  k.pairs = (int)a->pairs;
+  k.axes = (int)a->axes;
+  k.freqs = a->freqs;
+  k.pair_axis = a->pair_axis;
+  k.positions = a->positions;
+  k.rows_end = a->rows_end;
+  k.vec = vec;
+  set_last_path(vec ? "qk_norm_rope" : "qk_norm_rope_elements");
+  return ql::launch_qk_norm_rope(k, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? QL_OK : QL_EHIP;
+}
+
+QL_API int qlinear_rope_table_host(double theta, int64_t axes, const int64_t *pairs_per_axis, int order, float *freqs,
+                                   int32_t *axis) {
+  if (!(theta > 0) || !std::isfinite(theta) || axes < 1 || axes > kMaxHeads || !pairs_per_axis) return QL_EINVAL;
+  if (order != QL_ROPE_AXES_OWN && order != QL_ROPE_AXES_SHARED && order != QL_ROPE_AXES_TURNS) return QL_EINVAL;
+  int64_t pairs = 0, most = 0;
+  for (int64_t a = 0; a < axes; ++a) {
+    if (pairs_per_axis[a] < 0 || pairs_per_axis[a] > kMaxHeads) return QL_EINVAL;
+    pairs += pairs_per_axis[a];
+    most = std::max(most, pairs_per_axis[a]);
+  }
+  if (pairs > kMaxHeads) return QL_EINVAL;
+  if (pairs == 0) return QL_OK;
+  if (!freqs || !axis) return QL_EINVAL;
+  int64_t i = 0;
+  auto put = [&](int64_t a, int64_t j, int64_t n) {
+    freqs[i] = (float)std::pow(theta, -(double)j / (double)n);
+    axis[i++] = (int32_t)a;
+  };
+  if (order == QL_ROPE_AXES_TURNS) {
+    for (int64_t turn = 0; turn < most; ++turn)
+      for (int64_t a = 0; a < axes; ++a)
+        if (turn < pairs_per_axis[a]) put(a, i, pairs);
+  } else {
+    for (int64_t a = 0; a < axes; ++a)
+      for (int64_t j = 0; j < pairs_per_axis[a]; ++j)
+        if (order == QL_ROPE_AXES_OWN) put(a, j, pairs_per_axis[a]);
+        else put(a, i, pairs);
+  }
+  return QL_OK;
+}
+
+namespace {
+
+// Whether the sizes of an attention call are served: QL_OK, QL_EINVAL or QL_EUNSUPPORTED.
+int attention_sizes(int64_t Mq, int64_t Mk, int64_t samples, int64_t q_heads, int64_t kv_heads, int64_t D) {
+  if (Mq < 0 || Mk < 0 || samples < 0 || q_heads < 1 || kv_heads < 1 || D < 1) return QL_EINVAL;
+  if (q_heads > kMaxHeads || kv_heads > kMaxHeads) return QL_EUNSUPPORTED;
+  if (q_heads % kv_heads) return QL_EINVAL;
+  if (!head_dim_ok(D) || samples > kMaxSamples || Mk > kMaxAttentionRows ||
+      Mq > kMaxAttentionRows / (q_heads / kv_heads))
+    return QL_EUNSUPPORTED;
+  const ql::AttentionPlan p = ql::attention_plan(Mq, Mk, samples, (int)q_heads, (int)kv_heads, (int)D, true);
+  return p.blocks > kMaxBlocks ? QL_EUNSUPPORTED : QL_OK;
+}
+
+}  // namespace
+
+QL_API size_t qlinear_attention_workspace_bytes(int64_t Mq, int64_t Mk, int64_t samples, int64_t q_heads,
+                                                int64_t kv_heads, int64_t head_dim) {
+  if (attention_sizes(Mq, Mk, samples, q_heads, kv_heads, head_dim) != QL_OK || Mq == 0 || samples == 0) return 0;
+  return ql::attention_plan(Mq, Mk, samples, (int)q_heads, (int)kv_heads, (int)head_dim, true).partial_bytes;
+}
+
+QL_API int qlinear_attention(const ql_attention_args *a, void *stream) {
+  if (!a) return QL_EINVAL;
+  if ((a->q_offsets != nullptr) != (a->k_offsets != nullptr)) return QL_EINVAL;
+  const int64_t samples = a->q_offsets ? a->samples : 1;
+  const int st = attention_sizes(a->Mq, a->Mk, samples, a->q_heads, a->kv_heads, a->head_dim);
+  if (st != QL_OK) return st;
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return QL_EINVAL;
+  if (a->Mq == 0 || samples == 0) return QL_OK;
+  if (!a->q || !a->out || (a->Mk > 0 && (!a->k || !a->v))) return QL_EINVAL;
+  const int64_t q_row = a->q_heads * a->head_dim, kv_row = a->kv_heads * a->head_dim;
+  if (a->q_ld < q_row || a->out_ld < q_row || (a->Mk > 0 && (a->k_ld < kv_row || a->v_ld < kv_row))) return QL_EINVAL;
+  if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->out) || !aligned16(a->workspace) ||
+      !on_elements(a->q_offsets, 4) || !on_elements(a->k_offsets, 4) || a->q_ld % 8 || a->out_ld % 8 ||
+      (a->Mk > 0 && (a->k_ld % 8 || a->v_ld % 8)))
+    return QL_EALIGN;
+  if (a->q_ld > kMaxAttentionPitch || a->out_ld > kMaxAttentionPitch ||
+      (a->Mk > 0 && (a->k_ld > kMaxAttentionPitch || a->v_ld > kMaxAttentionPitch)))
+    return QL_EUNSUPPORTED;
+  const ql::AttentionPlan p = ql::attention_plan(a->Mq, a->Mk, samples, (int)a->q_heads, (int)a->kv_heads,
+                                                 (int)a->head_dim, a->workspace != nullptr);
+  if (a->workspace && a->workspace_bytes < p.partial_bytes) return QL_EWORKSPACE;
+  ql::AttentionArgs k{};
+  k.q = static_cast<const uint16_t *>(a->q);
+  k.k = static_cast<const uint16_t *>(a->k);
+  k.v = static_cast<const uint16_t *>(a->v);
+  k.out = static_cast<uint16_t *>(a->out);
+  k.q_ld = a->q_ld;
+  k.k_ld = a->Mk > 0 ? a->k_ld : 0;
+  k.v_ld = a->Mk > 0 ? a->v_ld : 0;
+  k.out_ld = a->out_ld;
+  k.Mq = a->Mq;
+  k.Mk = a->Mk;
+  k.kv_heads = (int)a->kv_heads;
+  k.group = (int)(a->q_heads / a->kv_heads);
+  k.D = (int)a->head_dim;
+  k.samples = (int)samples;
+  k.scale = a->scale;
+  k.q_offsets = a->q_offsets;
+  k.k_offsets = a->k_offsets;
+  k.key_mask = a->Mk > 0 ? a->key_mask : nullptr;
+  k.partial = static_cast<float *>(a->workspace);
+  char buf[160];
+  std::snprintf(buf, sizeof(buf), "attention_rows%d_slots%d", p.rows, p.slots);
+  set_last_path(buf);
+  return ql::launch_attention(k, p, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? QL_OK : QL_EHIP;
+}

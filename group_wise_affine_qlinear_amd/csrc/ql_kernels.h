@@ -196,4 +196,57 @@ struct AdapterPlan {
 AdapterPlan adapter_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t adapters);
 hipError_t launch_adapters(const AdapterArgs &a, const AdapterPlan &p, hipStream_t stream);
 
+// Head norms and rotation (heads.hip); fields as ql_qk_args, validated.
+struct HeadsArgs {
+  struct Part {
+    const void *in;
+    uint16_t *out;       // bf16
+    int64_t in_ld, out_ld;
+    const float *weight;  // [D] or null
+    int heads;           // 0: not in the call
+  } part[3];             // q, k, v
+  int64_t M;
+  int D;
+  int lane_bits;         // log2 of the lanes of a head: 8 << lane_bits >= D
+  int in_bf16;
+  int norm;              // ql_norm
+  float eps;
+  int pair_layout;       // ql_rope
+  int pairs, axes;
+  const float *freqs;
+  const int32_t *pair_axis, *positions, *rows_end;
+  int vec;               // everything on four elements
+};
+hipError_t launch_qk_norm_rope(const HeadsArgs &a, hipStream_t stream);
+
+// Attention (attention.hip); fields as ql_attention_args, validated.
+struct AttentionArgs {
+  const uint16_t *q, *k, *v;  // bf16
+  uint16_t *out;
+  int64_t q_ld, k_ld, v_ld, out_ld;
+  int64_t Mq, Mk;
+  int kv_heads, group;        // query heads per key head
+  int D;
+  int samples;
+  float scale;
+  const int32_t *q_offsets, *k_offsets;  // or null: one sample
+  const uint8_t *key_mask;               // or null
+  float *partial;                        // workspace
+  // set by launch_attention from the plan
+  int slots, cut_all, least_units;
+  int64_t pieces;
+};
+// How a call's tiles are divided over blocks, as far as the sizes alone say it.
+struct AttentionPlan {
+  int rows;              // query rows of a tile: 32, 128 or 256
+  int slots;             // blocks that the keys of cut tiles are divided over; 0: none is cut
+  int cut_all;           // 1: all tiles, 0: those behind the last multiple of slots
+  int least_units;       // units of keys of a piece at least
+  int64_t cut, pieces;   // cut tiles and their pieces at most
+  int64_t blocks;        // tiles and pieces at most
+  size_t partial_bytes;
+};
+AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, int q_heads, int kv_heads, int D, bool workspace);
+hipError_t launch_attention(const AttentionArgs &a, const AttentionPlan &p, hipStream_t stream);
+
 }  // namespace ql

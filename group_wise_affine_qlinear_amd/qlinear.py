@@ -25,6 +25,8 @@ QL_MODE_AUTO, QL_MODE_EXACT, QL_MODE_FAST, QL_MODE_SPLIT = 0, 1, 2, 3
 QL_EPI_NONE, QL_EPI_SWIGLU, QL_EPI_GATE_RESIDUAL = 0, 1, 2
 QL_NORM_NONE, QL_NORM_RMS, QL_NORM_LAYER = 0, 1, 2
 QL_ADAPTER_BF16, QL_ADAPTER_F16 = 0, 1
+QL_ROPE_HALVES, QL_ROPE_PAIRS = 0, 1
+QL_ROPE_AXES_OWN, QL_ROPE_AXES_SHARED, QL_ROPE_AXES_TURNS = 0, 1, 2
 
 EXPORTED = (
     "qlinear_forward", "qlinear_forward_ex", "qlinear_workspace_bytes", "qlinear_packed_words",
@@ -36,6 +38,7 @@ EXPORTED = (
     "qlinear_unrepack_glu", "qlinear_quantize_imatrix", "qlinear_forward_workspace_bytes",
     "qlinear_forward_noalloc", "qlinear_forward_noalloc_max_scratch",
     "qlinear_block_norm", "qlinear_adapters", "qlinear_adapters_workspace_bytes",
+    "qlinear_qk_norm_rope", "qlinear_rope_table_host", "qlinear_attention", "qlinear_attention_workspace_bytes",
 )
 
 
@@ -136,6 +139,64 @@ class ql_adapter_args(ctypes.Structure):
     ]
 
 
+class ql_qk_args(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64),
+        ("head_dim", ctypes.c_int64),
+        ("q_heads", ctypes.c_int64),
+        ("kv_heads", ctypes.c_int64),
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_ld", ctypes.c_int64),
+        ("k_ld", ctypes.c_int64),
+        ("v_ld", ctypes.c_int64),
+        ("in_dtype", ctypes.c_int),
+        ("q_out", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p),
+        ("v_out", ctypes.c_void_p),
+        ("q_out_ld", ctypes.c_int64),
+        ("k_out_ld", ctypes.c_int64),
+        ("v_out_ld", ctypes.c_int64),
+        ("norm", ctypes.c_int),
+        ("eps", ctypes.c_float),
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("rope", ctypes.c_int),
+        ("pairs", ctypes.c_int64),
+        ("freqs", ctypes.c_void_p),
+        ("pair_axis", ctypes.c_void_p),
+        ("axes", ctypes.c_int64),
+        ("positions", ctypes.c_void_p),
+        ("rows_end", ctypes.c_void_p),
+    ]
+
+
+class ql_attention_args(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("q_ld", ctypes.c_int64),
+        ("k_ld", ctypes.c_int64),
+        ("v_ld", ctypes.c_int64),
+        ("out_ld", ctypes.c_int64),
+        ("Mq", ctypes.c_int64),
+        ("Mk", ctypes.c_int64),
+        ("q_heads", ctypes.c_int64),
+        ("kv_heads", ctypes.c_int64),
+        ("head_dim", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("samples", ctypes.c_int64),
+        ("q_offsets", ctypes.c_void_p),
+        ("k_offsets", ctypes.c_void_p),
+        ("key_mask", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 _lib = None
 
 
@@ -187,6 +248,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "qlinear_block_norm": ([ctypes.POINTER(ql_block_norm_args), vp], i32),
         "qlinear_adapters": ([ctypes.POINTER(ql_adapter_args), vp], i32),
         "qlinear_adapters_workspace_bytes": ([i64, i64, i64, i64, i64], sz),
+        "qlinear_qk_norm_rope": ([ctypes.POINTER(ql_qk_args), vp], i32),
+        "qlinear_rope_table_host": ([ctypes.c_double, i64, vp, i32, vp, vp], i32),
+        "qlinear_attention": ([ctypes.POINTER(ql_attention_args), vp], i32),
+        "qlinear_attention_workspace_bytes": ([i64, i64, i64, i64, i64, i64], sz),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -736,7 +801,178 @@ def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, 
     return out
 
 
+# ------------------------------------------------------------------ between QKV and output projection
+
+def _heads(torch, t, name, dtypes, rows, D, device):
+    """(pointer, row pitch, heads) of a [rows, heads, D] tensor whose rows may be slices of longer ones."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != rows or shape[2] != D:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{rows}, heads, {D}]")
+    heads = shape[1]
+    pitch, head, step = t.stride()
+    width = heads * D
+    if rows > 0 and ((D > 1 and step != 1) or (heads > 1 and head != D) or (rows > 1 and pitch < width)):
+        raise ValueError(f"{name} must have rows of consecutive heads that do not overlap")
+    return t.data_ptr(), pitch if rows > 1 else width, heads
+
+
+def qlinear_qk_norm_rope(M, head_dim, *, q=None, k=None, v=None, q_out=None, k_out=None, v_out=None,
+                         norm=QL_NORM_NONE, eps=1e-6, q_weight=None, k_weight=None, rope=QL_ROPE_HALVES, freqs=None,
+                         pair_axis=None, positions=None, rows_end=None, stream=None):
+    """C ``qlinear_qk_norm_rope``: head norms and rotation between a QKV projection and attention.
+
+    ``q`` [M, q_heads, head_dim], ``k`` and ``v`` [M, kv_heads, head_dim], fp32 or bf16 (all the same), rows that
+    are slices of one projection output included; ``q_out``, ``k_out`` and ``v_out`` bf16 of the same shapes (may
+    be the bf16 inputs themselves). Each part may be left out, input and output together. Query and key heads
+    become N(x) * weight (``norm``, fp32 ``q_weight`` and ``k_weight`` [head_dim]), then pair i of the first
+    2 * len(``freqs``) values is turned by ``positions[pair_axis[i], m] * freqs[i]`` (``freqs`` fp32 in radians per
+    position, ``pair_axis`` int32, None: axis 0; ``positions`` int32 [axes, M] or [M]; without ``freqs`` nothing is
+    turned). Values are rounded to bf16. ``rows_end`` (int32, one element): rows from it on are left as they are.
+    """
+    torch = _torch()
+    lib = load_library()
+    first = next((t for t in (q, k, v) if t is not None), None)
+    if not isinstance(first, torch.Tensor):
+        raise TypeError("one of q, k and v must be a torch tensor")
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("q, k and v must be device tensors")
+    a = ql_qk_args()
+    a.M, a.head_dim, a.norm, a.eps, a.rope = M, head_dim, norm, eps, rope
+    a.in_dtype = _value_dtype(torch, first, "q, k and v")
+    one, bf16, f32, i32 = (first.dtype,), (torch.bfloat16,), (torch.float32,), (torch.int32,)
+    if q is not None:
+        a.q, a.q_ld, a.q_heads = _heads(torch, q, "q", one, M, head_dim, dev)
+        a.q_out, a.q_out_ld, heads = _heads(torch, q_out, "q_out", bf16, M, head_dim, dev)
+        if heads != a.q_heads:
+            raise ValueError("q_out must have the shape of q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k is not None:
+        a.k, a.k_ld, a.kv_heads = _heads(torch, k, "k", one, M, head_dim, dev)
+        a.k_out, a.k_out_ld, heads = _heads(torch, k_out, "k_out", bf16, M, head_dim, dev)
+        if heads != a.kv_heads:
+            raise ValueError("k_out must have the shape of k")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if v is not None:
+        a.v, a.v_ld, heads = _heads(torch, v, "v", one, M, head_dim, dev)
+        if k is not None and heads != a.kv_heads:
+            raise ValueError("k and v must have the same heads")
+        a.kv_heads = heads
+        a.v_out, a.v_out_ld, heads = _heads(torch, v_out, "v_out", bf16, M, head_dim, dev)
+        if heads != a.kv_heads:
+            raise ValueError("v_out must have the shape of v")
+    elif v_out is not None:
+        raise ValueError("v_out without v")
+    if q_weight is not None:
+        a.q_weight = _operand(q_weight, "q_weight", f32, (head_dim,), dev)
+    if k_weight is not None:
+        a.k_weight = _operand(k_weight, "k_weight", f32, (head_dim,), dev)
+    if freqs is not None:
+        a.pairs = freqs.shape[0] if isinstance(freqs, torch.Tensor) and freqs.dim() == 1 else 0
+        a.freqs = _operand(freqs, "freqs", f32, (a.pairs,), dev)
+        if not isinstance(positions, torch.Tensor):
+            raise TypeError("positions must be a torch tensor")
+        a.axes = positions.shape[0] if positions.dim() == 2 else 1
+        a.positions = _operand(positions, "positions", i32, (a.axes, M) if positions.dim() == 2 else (M,), dev)
+        if pair_axis is not None:
+            a.pair_axis = _operand(pair_axis, "pair_axis", i32, (a.pairs,), dev)
+    elif positions is not None or pair_axis is not None:
+        raise ValueError("positions and pair_axis need freqs")
+    if rows_end is not None:
+        if not isinstance(rows_end, torch.Tensor):
+            raise TypeError("rows_end must be a torch tensor")
+        if rows_end.numel() != 1:
+            raise ValueError("rows_end must be a tensor of one int32")
+        a.rows_end = _operand(rows_end, "rows_end", i32, rows_end.shape, dev)
+    _launch(torch, lib.qlinear_qk_norm_rope, "qlinear_qk_norm_rope", a, dev, stream)
+
+
+def qlinear_attention_workspace_bytes(Mq, Mk, samples, q_heads, kv_heads, head_dim) -> int:
+    return int(load_library().qlinear_attention_workspace_bytes(Mq, Mk, samples, q_heads, kv_heads, head_dim))
+
+
+def qlinear_attention(q, k, v, out, *, scale=None, q_offsets=None, k_offsets=None, key_mask=None,
+                      workspace=TORCH_WORKSPACE, stream=None):
+    """C ``qlinear_attention``: softmax attention of packed samples, over their own tokens or another sequence.
+
+    ``q`` and ``out`` bf16 [Mq, q_heads, D], ``k`` and ``v`` bf16 [Mk, kv_heads, D] (q_heads a multiple of
+    kv_heads), rows that are slices of longer ones included; ``scale`` is 1 / sqrt(D) by default. With
+    ``q_offsets`` and ``k_offsets`` (int32 [samples + 1]) the queries q_offsets[s] .. q_offsets[s + 1] see the
+    keys k_offsets[s] .. k_offsets[s + 1]; queries outside are left as they are. ``key_mask`` (bool or uint8
+    [Mk]) hides keys; a query without any gives zeros. ``workspace`` is a device tensor of
+    ``qlinear_attention_workspace_bytes`` bytes, ``None`` (keys are not cut into pieces), or by default one from
+    torch's caching allocator on the call's stream.
+    """
+    torch = _torch()
+    lib = load_library()
+    for t, name in ((q, "q"), (k, "k")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be a tensor [rows, heads, D]")
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("q must be a device tensor")
+    a = ql_attention_args()
+    bf16, i32 = (torch.bfloat16,), (torch.int32,)
+    a.Mq, a.Mk, a.head_dim = q.shape[0], k.shape[0], q.shape[2]
+    a.q, a.q_ld, a.q_heads = _heads(torch, q, "q", bf16, a.Mq, a.head_dim, dev)
+    a.k, a.k_ld, a.kv_heads = _heads(torch, k, "k", bf16, a.Mk, a.head_dim, dev)
+    a.v, a.v_ld, heads = _heads(torch, v, "v", bf16, a.Mk, a.head_dim, dev)
+    if heads != a.kv_heads:
+        raise ValueError("k and v must have the same heads")
+    a.out, a.out_ld, heads = _heads(torch, out, "out", bf16, a.Mq, a.head_dim, dev)
+    if heads != a.q_heads:
+        raise ValueError("out must have the shape of q")
+    a.scale = max(a.head_dim, 1) ** -0.5 if scale is None else scale
+    samples = 1
+    if (q_offsets is None) != (k_offsets is None):
+        raise ValueError("q_offsets and k_offsets must be given together")
+    if q_offsets is not None:
+        if not isinstance(q_offsets, torch.Tensor):
+            raise TypeError("q_offsets must be a torch tensor")
+        if q_offsets.dim() != 1 or q_offsets.shape[0] < 1:
+            raise ValueError("q_offsets must be a tensor [samples + 1]")
+        a.samples = samples = q_offsets.shape[0] - 1
+        a.q_offsets = _operand(q_offsets, "q_offsets", i32, q_offsets.shape, dev)
+        a.k_offsets = _operand(k_offsets, "k_offsets", i32, q_offsets.shape, dev)
+    if key_mask is not None:
+        a.key_mask = _operand(key_mask, "key_mask", (torch.bool, torch.uint8), (a.Mk,), dev)
+    if isinstance(workspace, str):
+        if workspace != TORCH_WORKSPACE:
+            raise ValueError(f"workspace must be a device tensor, None or {TORCH_WORKSPACE!r}")
+        nbytes = lib.qlinear_attention_workspace_bytes(a.Mq, a.Mk, samples, a.q_heads, a.kv_heads, a.head_dim)
+        workspace = _empty(torch, nbytes, torch.uint8, dev, stream) if nbytes else None
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError(f"workspace must be a device tensor, None or {TORCH_WORKSPACE!r}")
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        a.workspace = workspace.data_ptr()
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+    _launch(torch, lib.qlinear_attention, "qlinear_attention", a, dev, stream)
+    return out
+
+
 # ------------------------------------------------------------------ host entry points
+
+def qlinear_rope_table_host(theta, pairs_per_axis, order=QL_ROPE_AXES_OWN):
+    """C ``qlinear_rope_table_host``: (freqs fp32, axis int32) arrays for ``qlinear_qk_norm_rope``."""
+    n = np.ascontiguousarray(pairs_per_axis, dtype=np.int64)
+    pairs = max(int(n.sum()), 0)
+    freqs, axis = np.empty(pairs, dtype=np.float32), np.empty(pairs, dtype=np.int32)
+    _check(load_library().qlinear_rope_table_host(theta, n.size, n.ctypes.data, order, freqs.ctypes.data, axis.ctypes.data),
+           "qlinear_rope_table_host")
+    return freqs, axis
+
 
 def qlinear_packed_words(bits, N, K) -> int:
     return int(load_library().qlinear_packed_words(bits, N, K))

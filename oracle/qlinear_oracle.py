@@ -82,7 +82,7 @@ __all__ = [
     "fast_weights_f16", "fast_activations_f16", "forward_fast", "forward_fast_rows", "silu", "swiglu",
     "gate_residual", "adaln_modulate", "forward_modulated",
     "IMATRIX_DELTAS", "quantize_imatrix", "weighted_error",
-    "norm_rows", "block_norm", "adapter_delta",
+    "norm_rows", "block_norm", "adapter_delta", "rotate_heads", "qk_norm_rope", "attention",
 ]
 
 GROUP = 64
@@ -580,3 +580,52 @@ def adapter_delta(x, a, b, row_adapter, ranks=None, scaling=None) -> np.ndarray:
         v = a[i, :r] @ x[m]
         out[m] = (1.0 if scaling is None else float(scaling[i])) * (b[i, :, :r] @ v)
     return out
+
+
+def rotate_heads(u, positions, freqs, pair_axis=None, layout="halves") -> np.ndarray:
+    """[M, heads, D] in fp64, pair i of the first 2 len(freqs) values turned by positions[pair_axis[i], m] * freqs[i];
+    "halves": pairs (i, i + len(freqs)), "pairs": (2i, 2i + 1). A pair of an axis that is not there is not turned."""
+    u = np.array(u, dtype=np.float64)
+    positions = np.atleast_2d(np.asarray(positions, dtype=np.int64))
+    n = len(freqs)
+    for i in range(n):
+        axis = 0 if pair_axis is None else int(pair_axis[i])
+        if not 0 <= axis < positions.shape[0]:
+            continue
+        t = (positions[axis].astype(np.float64) * np.float64(freqs[i]))[:, None]
+        x, y = (i, i + n) if layout == "halves" else (2 * i, 2 * i + 1)
+        a, b = u[..., x].copy(), u[..., y].copy()
+        u[..., x], u[..., y] = a * np.cos(t) - b * np.sin(t), b * np.cos(t) + a * np.sin(t)
+    return u
+
+
+def qk_norm_rope(x, weight=None, norm="none", eps=1e-6, positions=None, freqs=(), pair_axis=None,
+                 layout="halves") -> np.ndarray:
+    """Heads of [M, heads, D] normalised, weighted and turned, in fp64."""
+    x = np.asarray(x, dtype=np.float64)
+    u = norm_rows(x.reshape(-1, x.shape[-1]), norm, eps).reshape(x.shape)
+    if weight is not None:
+        u = u * np.asarray(weight, dtype=np.float64)
+    return rotate_heads(u, positions, freqs, pair_axis, layout) if len(freqs) else u
+
+
+def attention(q, k, v, scale, q_offsets=None, k_offsets=None, key_mask=None):
+    """(out, live) in fp64: softmax attention of packed samples, q [Mq, Hq, D] over k, v [Mk, Hkv, D]; live marks the
+    queries that belong to a sample. A query without a kept key gives zeros."""
+    q = np.asarray(q, dtype=np.float64)
+    out, live = np.zeros_like(q), np.zeros(q.shape[0], dtype=bool)
+    if q_offsets is None:
+        q_offsets, k_offsets = [0, q.shape[0]], [0, len(k)]
+    group = q.shape[1] // k.shape[1]
+    for q0, q1, k0, k1 in zip(q_offsets[:-1], q_offsets[1:], k_offsets[:-1], k_offsets[1:]):
+        live[q0:q1] = True
+        keys = np.arange(k0, k1)
+        if key_mask is not None:
+            keys = keys[np.asarray(key_mask)[k0:k1] != 0]
+        if q1 == q0 or len(keys) == 0:
+            continue
+        for h in range(q.shape[1]):
+            s = scale * (q[q0:q1, h] @ np.asarray(k[keys, h // group], dtype=np.float64).T)
+            p = np.exp(s - s.max(axis=1, keepdims=True))
+            out[q0:q1, h] = p @ np.asarray(v[keys, h // group], dtype=np.float64) / p.sum(axis=1, keepdims=True)
+    return out, live
