@@ -20,18 +20,14 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["gemm3.hip", "gemm3o.hip", "gemm4.hip", "gemm2.hip", "host.cpp", "gemm.hip", "skinny.hip", "gemv.hip", "misc.hip",
            "layout.hip", "norm.hip", "adapters.hip", "heads.hip", "attention.hip"]
 
-# MFMA results in VGPRs: the per-group fp32 epilogue reads them with VALU ops
-VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-# sources whose accumulators alone fill the 256 VGPRs and belong in AGPRs
-AGPR_SOURCES = ("attention.hip",)
-
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",
     "--offload-arch=gfx950",
     # packed-fp32 VALU instructions stay off: plain float code only
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
-    *VGPR_FORM,
+    # MFMA results in VGPRs: the per-group fp32 epilogue reads them with VALU ops
+    "-mllvm", "-amdgpu-mfma-vgpr-form=1",
     "-I", os.path.join(ROOT, "include"),
 ]
 
@@ -43,14 +39,9 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
-def source_flags(src: str) -> list[str]:
-    """Flags that a source is compiled with."""
-    return [f for f in COMMON_FLAGS if f not in VGPR_FORM] if src in AGPR_SOURCES else COMMON_FLAGS
-
-
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [hipcc(), *source_flags(src), "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [hipcc(), *COMMON_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
     if src.endswith(".cpp"):
         cmd[1:1] = ["-x", "hip"]
     res = subprocess.run(cmd, capture_output=True, text=True)

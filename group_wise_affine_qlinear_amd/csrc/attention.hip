@@ -17,6 +17,7 @@
 // rounded weights, so that what the output is divided by is exactly what it
 // was multiplied by. The output is rounded once.
 #include <algorithm>
+#include <utility>
 
 #include "ql_block.h"
 #include "ql_kernels.h"
@@ -76,6 +77,11 @@ __device__ __forceinline__ Sample sample_of(const AttentionArgs &a, int s) {
   return r;
 }
 
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // Inclusive sum over the 64 lanes.
 __device__ __forceinline__ int64_t scan(int64_t v) {
 #pragma unroll
@@ -125,6 +131,7 @@ struct Division {
       p.tiles += __shfl(scan(tiles_of(a, x)), 63);
       return false;
     });
+    p.tiles = uniform(p.tiles);
     if (a.slots == 0) {
       p.whole = p.tiles;
       return p;
@@ -138,7 +145,7 @@ struct Division {
       first += __shfl(incl, 63);
       return false;
     });
-    p.per = (int)max((units + a.slots - 1) / a.slots, (int64_t)a.least_units);
+    p.per = (int)max((uniform(units) + a.slots - 1) / a.slots, (int64_t)a.least_units);
     return p;
   }
 
@@ -179,7 +186,17 @@ struct Division {
       pieces += __shfl(pincl, 63);
       return false;
     });
-    return found;
+    // the same in every lane: addresses made of it stay scalar
+    w.s.q0 = uniform(w.s.q0);
+    w.s.k0 = uniform(w.s.k0);
+    w.s.rows = __builtin_amdgcn_readfirstlane(w.s.rows);
+    w.s.keys = __builtin_amdgcn_readfirstlane(w.s.keys);
+    w.head = __builtin_amdgcn_readfirstlane(w.head);
+    w.tile = __builtin_amdgcn_readfirstlane(w.tile);
+    w.unit0 = __builtin_amdgcn_readfirstlane(w.unit0);
+    w.unit1 = __builtin_amdgcn_readfirstlane(w.unit1);
+    w.slot = uniform(w.slot);
+    return __builtin_amdgcn_readfirstlane(found);
   }
 };
 
@@ -196,15 +213,18 @@ __device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t n) {
 __device__ __forceinline__ constexpr int acc_row(int r) { return (r >> 2) * 8 + (r & 3); }
 
 template <int DP, int NQ>
-struct State {
+struct Queries {
   bf16x8 q[NQ][DP / 16];     // Q^T: lane's query, 8 values at 16 i + 8 (lane / 32)
-  f32x16 o[NQ][DP / 32];     // O^T
   float m[NQ], l[NQ];        // maximum followed (in powers of two), sum of this half's weights
+};
+template <int DP, int NQ>
+struct State : Queries<DP, NQ> {
+  f32x16 o[NQ][DP / 32];     // O^T
 };
 
 // Query rows r0 + 32 i + (lane & 31) of a tile into registers; zeros past the rows and past D.
 template <int DP, int NQ>
-__device__ __forceinline__ void load_q(const AttentionArgs &a, const Work &w, int r0, State<DP, NQ> &st) {
+__device__ __forceinline__ void load_q(const AttentionArgs &a, const Work &w, int r0, Queries<DP, NQ> &st) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
@@ -219,8 +239,6 @@ __device__ __forceinline__ void load_q(const AttentionArgs &a, const Work &w, in
       if (in && d < a.D) v = *reinterpret_cast<const u32x4 *>(p + d);
       st.q[i][j] = as_bf16x8(v);
     }
-#pragma unroll
-    for (int j = 0; j < DP / 32; ++j) st.o[i][j] = f32x16{};
     st.m[i] = kLowest;
     st.l[i] = 0.f;
   }
@@ -229,12 +247,15 @@ __device__ __forceinline__ void load_q(const AttentionArgs &a, const Work &w, in
 // S^T of 32 keys: K rows [row0, row0 + 32) of the stage at kb.
 template <int DP, int NQ>
 __device__ __forceinline__ void scores(const unsigned char *kb, int row0, const State<DP, NQ> &st, f32x16 (&s)[NQ]) {
-  const int lane = threadIdx.x & 63, row = row0 + (lane & 31), h = lane >> 5;
+  const int lane = threadIdx.x & 63, row = lane & 31, h = lane >> 5;
 #pragma unroll
   for (int i = 0; i < NQ; ++i) s[i] = f32x16{};
+  int base[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) base[j] = row * (DP * 2) + k_unit(row, 2 * j + h) * 16;
 #pragma unroll
   for (int j = 0; j < DP / 16; ++j) {
-    const bf16x8 k = lds_read8(kb + row * (DP * 2) + k_unit(row, 2 * j + h) * 16);
+    const bf16x8 k = lds_read8(kb + base[j & 3] + (row0 * DP * 2 + (j >> 2) * 128));
 #pragma unroll
     for (int i = 0; i < NQ; ++i) s[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, st.q[i][j], s[i], 0, 0, 0);
   }
@@ -299,13 +320,16 @@ __device__ __forceinline__ void weights(State<DP, NQ> &st, f32x16 (&s)[NQ], floa
 template <int DP, int NQ>
 __device__ __forceinline__ void outputs(const unsigned char *vb, int row0, State<DP, NQ> &st, const bf16x8 (&p)[NQ][2]) {
   const int lane = threadIdx.x & 63, h = lane >> 5;
-  const int row = row0 + 4 * h + ((lane & 15) >> 2);                  // + 16 t + 8 u
+  const int row = 4 * h + ((lane & 15) >> 2);                         // + 16 t + 8 u
   const int unit = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), byte = (lane & 1) * 8;  // + 4 j
+  int base[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) base[j] = row * (DP * 2) + v_unit(row, unit + 4 * j) * 16 + byte;
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int j = 0; j < DP / 32; ++j) {
-      const unsigned char *r = vb + (row + 16 * t) * (DP * 2) + v_unit(row, unit + 4 * j) * 16 + byte;
+      const unsigned char *r = vb + base[j & 1] + ((row0 + 16 * t) * DP * 2 + (j >> 1) * 128);
       const s16x4 lo = lds_read_tr(r), hi = lds_read_tr(r + 8 * DP * 2);
       const bf16x8 v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
@@ -317,7 +341,11 @@ __device__ __forceinline__ void outputs(const unsigned char *vb, int row0, State
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const AttentionArgs &a, const uint16_t *x, int64_t ld,
                                                           const Work &w, int first) {
   const int64_t rows = w.s.keys - first;
-  return make_rsrc(x + (w.s.k0 + first) * ld + (int64_t)w.head * a.D, 0, rows <= 0 ? 0 : ((rows - 1) * ld + a.D) * 2);
+  const uint16_t *p = x + (w.s.k0 + first) * ld + (int64_t)w.head * a.D;
+  // said to be the same in every lane here again: a resource that the compiler
+  // takes for the lanes' own makes every copy a loop over the lanes
+  return make_rsrc(reinterpret_cast<const void *>(uniform(reinterpret_cast<int64_t>(p))), 0,
+                   uniform(rows <= 0 ? 0 : ((rows - 1) * ld + a.D) * 2));
 }
 
 // Bits of the keys [first, first + 64) of the sample that are kept.
@@ -347,116 +375,332 @@ __device__ __forceinline__ float reciprocal(float l) { return l == 0.f ? 0.f : 1
 
 // ------------------------------------------------------------------ tiles of many rows
 
-// A block of four waves, 32 NQ rows each, over keys in stages of 64 that all
-// waves read from LDS, the next stage on its way meanwhile.
+// Bytes of a wave's LDS reads: where a lane finds its part of fragment j of 32
+// K rows (16 bytes) and of V^T (twice eight bytes). The unit of a row moves in
+// bits that repeat every four (two) fragments, so that few bases and constant
+// offsets serve all of them.
+template <int DP>
+struct Lanes {
+  int k[4], v[2];
+
+  __device__ __forceinline__ Lanes() {
+    const int lane = threadIdx.x & 63, h = lane >> 5, row = lane & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = row * (DP * 2) + k_unit(row, 2 * j + h) * 16;
+    const int vrow = 4 * h + ((lane & 15) >> 2), unit = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) v[j] = vrow * (DP * 2) + v_unit(vrow, unit + 4 * j) * 16 + (lane & 1) * 8;
+  }
+  // 16 values of K's row at 16 j, of the 32 rows at kb
+  __device__ __forceinline__ bf16x8 k_frag(const unsigned char *kb, int j) const {
+    return lds_read8(kb + k[j & 3] + (j >> 2) * 128);
+  }
+  // V^T's rows 32 (f % (DP / 32)), of 16 of the 32 keys at vb
+  __device__ __forceinline__ bf16x8 v_frag(const unsigned char *vb, int f) const {
+    const int t = f / (DP / 32), j = f % (DP / 32);
+    const unsigned char *p = vb + v[j & 1] + (16 * t * DP * 2 + (j >> 1) * 128);
+    const s16x4 lo = lds_read_tr(p), hi = lds_read_tr(p + 8 * DP * 2);
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+};
+
+// Accumulators of attention_kernel: tile n (32 values of 32 queries) is in the
+// AGPRs a[16 n .. 16 n + 15], named in the instructions themselves. With 64
+// queries of 256 values they are all 256 AGPRs of a wave that has a SIMD's
+// registers to itself; held as variables, every branch that they live across
+// would need free ones to move them through, and the compiler sends hundreds
+// of them through scratch memory instead. Nothing else in the kernel uses
+// AGPRs: the scores' products are built into VGPRs, and the clobbers keep the
+// compiler's own values out (tests/test_qk_attention_host.py looks through the
+// assembly for any other use).
+#define QL_D(n) "a" #n "0", "a" #n "1", "a" #n "2", "a" #n "3", "a" #n "4", "a" #n "5", "a" #n "6", "a" #n "7", "a" #n "8", "a" #n "9"
+#define QL_ACC64 "a0", "a1", "a2", "a3", "a4", "a5", "a6", "a7", "a8", "a9", QL_D(1), QL_D(2), QL_D(3), QL_D(4), QL_D(5), \
+    "a60", "a61", "a62", "a63"
+#define QL_ACC128 QL_ACC64, "a64", "a65", "a66", "a67", "a68", "a69", QL_D(7), QL_D(8), QL_D(9), QL_D(10), QL_D(11), "a120", \
+    "a121", "a122", "a123", "a124", "a125", "a126", "a127"
+#define QL_ACC256 QL_ACC128, "a128", "a129", QL_D(13), QL_D(14), QL_D(15), QL_D(16), QL_D(17), QL_D(18), QL_D(19), QL_D(20), \
+    QL_D(21), QL_D(22), QL_D(23), QL_D(24), "a250", "a251", "a252", "a253", "a254", "a255"
+// An instruction on the accumulators of a kernel of TILES tiles.
+#define QL_ACC_ASM(TILES, ...)                                        \
+  if constexpr ((TILES) <= 4) asm volatile(__VA_ARGS__ : QL_ACC64);   \
+  else if constexpr ((TILES) <= 8) asm volatile(__VA_ARGS__ : QL_ACC128); \
+  else asm volatile(__VA_ARGS__ : QL_ACC256)
+
+template <int TILES>
+struct Acc {
+  // Waits before an accumulator is read or written by anything but a product (a product takes 16 passes).
+  static __device__ __forceinline__ void settle() { QL_ACC_ASM(TILES, "s_nop 15\n\ts_nop 7" : :); }
+
+  // Tile N += a b. The wait covers an operand that a VALU instruction wrote just before.
+  template <int N> static __device__ __forceinline__ void mfma(bf16x8 a, bf16x8 b) {
+    QL_ACC_ASM(TILES, "s_nop 1\n\tv_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, a[%2:%3]"
+               : : "v"(a), "v"(b), "n"(16 * N), "n"(16 * N + 15));
+  }
+  template <int R = 0> static __device__ __forceinline__ void clear() {
+    if constexpr (R < 16 * TILES) {
+      QL_ACC_ASM(TILES, "v_accvgpr_write_b32 a[%0], 0\n\tv_accvgpr_write_b32 a[%1], 0\n\tv_accvgpr_write_b32 a[%2], 0\n\t"
+                 "v_accvgpr_write_b32 a[%3], 0" : : "n"(R), "n"(R + 1), "n"(R + 2), "n"(R + 3));
+      clear<R + 4>();
+    }
+  }
+  // Four values of tile N, from register R on. The waits: settle() first.
+  template <int N, int R> static __device__ __forceinline__ f32x4 get() {
+    float a, b, c, d;
+    QL_ACC_ASM(TILES, "v_accvgpr_read_b32 %0, a[%4]\n\tv_accvgpr_read_b32 %1, a[%5]\n\tv_accvgpr_read_b32 %2, a[%6]\n\t"
+               "v_accvgpr_read_b32 %3, a[%7]" : "=v"(a), "=v"(b), "=v"(c), "=v"(d)
+               : "n"(16 * N + R), "n"(16 * N + R + 1), "n"(16 * N + R + 2), "n"(16 * N + R + 3));
+    return f32x4{a, b, c, d};
+  }
+  // Tiles FIRST .. LAST - 1 times f. settle() first; the wait at the end is for the next product.
+  template <int FIRST, int LAST> static __device__ __forceinline__ void scale(float f) {
+    if constexpr (FIRST < LAST) {
+      scale4<16 * FIRST>(f);
+      scale<FIRST + 1, LAST>(f);
+    }
+  }
+  template <int R> static __device__ __forceinline__ void scale4(float f) {
+    float a, b, c, d;
+    QL_ACC_ASM(TILES, "v_accvgpr_read_b32 %0, a[%5]\n\tv_accvgpr_read_b32 %1, a[%6]\n\tv_accvgpr_read_b32 %2, a[%7]\n\t"
+               "v_accvgpr_read_b32 %3, a[%8]\n\tv_mul_f32 %0, %0, %4\n\tv_mul_f32 %1, %1, %4\n\tv_mul_f32 %2, %2, %4\n\t"
+               "v_mul_f32 %3, %3, %4\n\tv_accvgpr_write_b32 a[%5], %0\n\tv_accvgpr_write_b32 a[%6], %1\n\t"
+               "v_accvgpr_write_b32 a[%7], %2\n\tv_accvgpr_write_b32 a[%8], %3\n\ts_nop 1"
+               : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d) : "v"(f), "n"(R), "n"(R + 1), "n"(R + 2), "n"(R + 3));
+    if constexpr (R % 16 != 12) scale4<R + 4>(f);
+  }
+};
+
+template <int N> struct Count { static constexpr int value = N; };
+
+// f(Count<0>), ..., f(Count<N - 1>): accumulators are named by constants.
+template <int... I, typename F>
+__device__ __forceinline__ void constants(std::integer_sequence<int, I...>, F f) { (f(Count<I>{}), ...); }
+template <int N, typename F>
+__device__ __forceinline__ void constants(F f) { constants(std::make_integer_sequence<int, N>{}, f); }
+
+// A block of four waves, 32 NQ rows each, over keys in chunks of 32 that all
+// waves read from LDS.
+//
+// While the scores of chunk i + 1 are multiplied, those of chunk i become
+// weights between the MFMAs; while these meet V, the next maximum is taken.
 template <int DP, int NQ, bool MASKED>
 __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
-  constexpr int BQ = 128 * NQ, UNIT = 64, kBytes = UNIT * DP * 2;
-  constexpr int kUnits = DP / 8;             // 16-byte units of a row
+  constexpr int BQ = 128 * NQ, UNIT = 64, kBytes = UNIT * DP * 2, kHalf = kBytes / 2;
+  constexpr int kUnits = DP / 8;                // 16-byte units of a row
   constexpr int kCopies = UNIT * kUnits / 256;  // copies of 64 units per wave and stage
+  constexpr int kSteps = DP / 16, kFrags = DP / 16;
   __shared__ __attribute__((aligned(16))) unsigned char k0[kBytes], k1[kBytes], v0[kBytes], v1[kBytes];
   using Div = Division<BQ, UNIT>;
   const Plan plan = Div::plan(a);
   Work w;
-  if ((int64_t)blockIdx.x < plan.whole) {
-    if (!Div::find(a, plan, xcd_order(blockIdx.x, plan.whole), 0, w)) return;
-  } else {
-    if (!Div::find(a, plan, -1, blockIdx.x - plan.whole, w)) return;
-  }
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const bool is_whole = (int64_t)blockIdx.x < plan.whole;
+  if (!Div::find(a, plan, is_whole ? xcd_order(blockIdx.x, plan.whole) : -1, (int64_t)blockIdx.x - plan.whole, w)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, h = lane >> 5;
   const int r0 = w.tile * BQ + wave * 32 * NQ;
-  const bool busy = r0 < w.s.rows;
-  State<DP, NQ> st;
+  using O = Acc<NQ * DP / 32>;
+  constexpr int kTiles = DP / 32;  // of a query block
+  Queries<DP, NQ> st;
   load_q<DP, NQ>(a, w, r0, st);
   const float c = a.scale * 1.4426950408889634f;
+  const Lanes<DP> at;
 
   // copy i of this wave: unit (4 i + wave) * 64 + lane of the stage
-  int row[kCopies], kofs[kCopies], vofs[kCopies];
-#pragma unroll
-  for (int i = 0; i < kCopies; ++i) {
-    const int id = (4 * i + wave) * 64 + lane;
-    row[i] = id / kUnits;
-    const int kc = k_unit(row[i], id % kUnits), vc = v_unit(row[i], id % kUnits);
-    kofs[i] = kc * 8 < a.D ? (int)(row[i] * a.k_ld + kc * 8) * 2 : kOut;
-    vofs[i] = vc * 8 < a.D ? (int)(row[i] * a.v_ld + vc * 8) * 2 : kOut;
-  }
-  int next_mask = 0;
-  auto copy = [&](unsigned char *kb, unsigned char *vb, int first, uint64_t keep) {
-    const auto kr = rows_of(a, a.k, a.k_ld, w, first), vr = rows_of(a, a.v, a.v_ld, w, first);
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const bool in = !MASKED || (keep >> row[i] & 1);
-      dma16(kr, in ? kofs[i] : kOut, 0, kb + (4 * i + wave) * 1024);
-    }
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const bool in = !MASKED || (keep >> row[i] & 1);
-      dma16(vr, in ? vofs[i] : kOut, 0, vb + (4 * i + wave) * 1024);
-    }
-  };
+  constexpr int kRows = 256 / kUnits;  // rows from copy to copy, a multiple of 8: the units of a lane stay
+  const int row = (wave * 64 + lane) / kUnits;
+  const int kc = k_unit(row, lane % kUnits), vc = v_unit(row, lane % kUnits);
+  const int kofs = kc * 8 < a.D ? (int)(row * a.k_ld + kc * 8) * 2 : kOut;
+  const int vofs = vc * 8 < a.D ? (int)(row * a.v_ld + vc * 8) * 2 : kOut;
   const int first = w.unit0 * UNIT, end = min(w.unit1 * UNIT, w.s.keys);
-  uint64_t keep = 0, keep_next = 0;
-  auto stage = [&](unsigned char *kb, unsigned char *vb, unsigned char *kn, unsigned char *vn, int at) {
-    dma_barrier();  // this stage has landed everywhere, the one before is free
-    keep = keep_next;
-    if (at + UNIT < end) {
-      keep_next = kept<MASKED>(a, w, at + UNIT, next_mask);
-      if constexpr (MASKED) next_mask = mask_byte(a, w, at + 2 * UNIT);
-      copy(kn, vn, at + UNIT, keep_next);
-    }
-    if (!busy || keep == 0) return;
+  auto copy = [&](const uint16_t *x, int64_t ld, int ofs, unsigned char *to, int from, uint64_t keep) __attribute__((always_inline)) {
+    const auto r = rows_of(a, x, ld, w, from);
+    const uint32_t step = (uint32_t)(kRows * ld * 2);
+    uint32_t o = ofs;
+    asm volatile("" : "+v"(o));  // or every copy's offset is kept in a register over the loop
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      f32x16 s[NQ];
-      bf16x8 p[NQ][2];
-      scores<DP, NQ>(kb, 32 * t, st, s);
-      weights<DP, NQ>(st, s, c, (uint32_t)(keep >> (32 * t)), p);
-      outputs<DP, NQ>(vb, 32 * t, st, p);
+    for (int i = 0; i < kCopies; ++i)
+      dma16(r, !MASKED || (keep >> (row + i * kRows) & 1) ? o + i * step : kOut, 0, to + (4 * i + wave) * 1024);
+  };
+  // Kept keys of the stages in hand; a stage's bytes of the mask are requested two stages ahead.
+  uint64_t keep = 0, keep1 = 0;
+  int byte = 0;
+  auto next_keep = [&](int from) __attribute__((always_inline)) {
+    const uint64_t k = kept<MASKED>(a, w, from, byte);
+    if constexpr (MASKED) byte = mask_byte(a, w, from + UNIT);
+    return k;
+  };
+
+  f32x16 s[2][NQ];
+  // The maximum of a chunk's scores is followed if it has grown by more than the slack, each query's by its own alone.
+  auto follow = [&](float (&mx)[NQ]) __attribute__((always_inline)) {
+    bool grown = false;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      mx[i] = fmaxf(mx[i], other_half(mx[i])) * c;
+      grown |= mx[i] > st.m[i] + kSlack;
+    }
+    if (!__any(grown)) return;
+    O::settle();
+    float f[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const float m = mx[i] > st.m[i] + kSlack ? mx[i] : st.m[i];
+      f[i] = __builtin_amdgcn_exp2f(st.m[i] - m);
+      st.m[i] = m;
+      st.l[i] *= f[i];
+    }
+    O::template scale<0, kTiles>(f[0]);
+    if constexpr (NQ == 2) O::template scale<kTiles, 2 * kTiles>(f[1]);
+  };
+  auto hide = [&](f32x16 (&x)[NQ], uint32_t valid) __attribute__((always_inline)) {
+    if (valid == 0xFFFFFFFFu) return;
+    const uint32_t mine = valid >> (4 * h);
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) x[i][r] = (mine >> acc_row(r)) & 1 ? x[i][r] : -__builtin_inff();
+  };
+  auto scores_of = [&](const unsigned char *kb, f32x16 (&x)[NQ]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) x[i] = f32x16{};
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+      const bf16x8 k = at.k_frag(kb, j);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) x[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, st.q[i][j], x[i], 0, 0, 0);
     }
   };
-  if (first < end) {
-    if constexpr (MASKED) next_mask = mask_byte(a, w, first);
-    keep_next = kept<MASKED>(a, w, first, next_mask);
-    if constexpr (MASKED) next_mask = mask_byte(a, w, first + UNIT);
-    copy(k0, v0, first, keep_next);
-    for (int at = first; at < end; at += 2 * UNIT) {
-      stage(k0, v0, k1, v1, at);
-      if (at + UNIT < end) stage(k1, v1, k0, v0, at + UNIT);
-    }
-  }
-  if (!busy) return;
-  const int h = lane >> 5;
-  float *part = w.slot >= 0 ? slot_at<DP, BQ>(a, w.slot) : nullptr;
+  auto largest = [&](f32x16 (&x)[NQ], float (&mx)[NQ]) __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < NQ; ++i) {
+    for (int i = 0; i < NQ; ++i) {
+      mx[i] = x[i][0];
+#pragma unroll
+      for (int r = 1; r < 16; ++r) mx[i] = fmaxf(mx[i], x[i][r]);
+    }
+  };
+
+  // One chunk: its scores `x` meet V's rows at vb; meanwhile the next chunk's
+  // become y (K rows at kb, kept keys `valid`).
+  auto chunk = [&](const unsigned char *kb, const unsigned char *vb, f32x16 (&x)[NQ], f32x16 (&y)[NQ], uint32_t valid) __attribute__((always_inline)) {
+    uint32_t p[NQ][8];
+    constexpr int kPairs = NQ * 8;
+    auto pair = [&](int e) __attribute__((always_inline)) {  // weights 2 (e % 8) and the next of query block e / 8
+      const int i = e / 8, r = e % 8 * 2;
+      p[i][r / 2] = pack_bf16(__builtin_amdgcn_exp2f(__builtin_fmaf(x[i][r], c, -st.m[i])),
+                              __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][r + 1], c, -st.m[i])));
+      const bf16x2 one = {(__bf16)1.f, (__bf16)1.f};
+      st.l[i] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p[i][r / 2]), one, st.l[i], false);
+      asm volatile("" : "+v"(p[i][r / 2]), "+v"(st.l[i]));  // stays between the MFMAs where it is placed
+    };
+    bf16x8 kf[3];
+    kf[0] = at.k_frag(kb, 0);
+    kf[1] = at.k_frag(kb, 1);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) y[i] = f32x16{};
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+      if (j + 2 < kSteps) kf[(j + 2) % 3] = at.k_frag(kb, j + 2);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) y[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[j % 3], st.q[i][j], y[i], 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < (kPairs + kSteps - 1) / kSteps; ++u)
+        if (j * kPairs / kSteps + u < (j + 1) * kPairs / kSteps) pair(j * kPairs / kSteps + u);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    hide(y, valid);
+    bf16x8 vf[3];
+    vf[0] = at.v_frag(vb, 0);
+    vf[1] = at.v_frag(vb, 1);
+    float mx[NQ];
+    __builtin_amdgcn_sched_barrier(0);
+    constants<kFrags>([&](auto count) __attribute__((always_inline)) {
+      constexpr int f = decltype(count)::value, t = f / kTiles, j = f % kTiles;
+      if constexpr (f + 2 < kFrags) vf[(f + 2) % 3] = at.v_frag(vb, f + 2);
+      O::template mfma<j>(vf[f % 3], as_bf16x8(u32x4{p[0][4 * t], p[0][4 * t + 1], p[0][4 * t + 2], p[0][4 * t + 3]}));
+      if constexpr (NQ == 2)
+        O::template mfma<kTiles + j>(vf[f % 3], as_bf16x8(u32x4{p[1][4 * t], p[1][4 * t + 1], p[1][4 * t + 2], p[1][4 * t + 3]}));
+#pragma unroll
+      for (int r = f * 16 / kFrags; r < (f + 1) * 16 / kFrags; ++r)
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) mx[i] = r ? fmaxf(mx[i], y[i][r]) : y[i][0];
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    follow(mx);
+  };
+  // All but the `ahead` newest of this wave's copies have landed, and so have the other waves'.
+  auto landed = [&](auto ahead) __attribute__((always_inline)) {
+    constexpr int n = decltype(ahead)::value;
+    __builtin_amdgcn_s_waitcnt((n & 0xF) | ((n >> 4) << 14) | 0xF70);
+    __syncthreads();
+  };
+
+  O::clear();
+  if (first < end) {
+    if constexpr (MASKED) byte = mask_byte(a, w, first);
+    keep = next_keep(first);
+    keep1 = next_keep(first + UNIT);
+    copy(a.k, a.k_ld, kofs, k0, first, keep);
+    copy(a.v, a.v_ld, vofs, v0, first, keep);
+    copy(a.k, a.k_ld, kofs, k1, first + UNIT, keep1);
+    __builtin_amdgcn_s_waitcnt(((2 * kCopies) & 0xF) | (((2 * kCopies) >> 4) << 14) | 0xF70);
+    __syncthreads();
+    scores_of(k0, s[0]);
+    hide(s[0], (uint32_t)keep);
+    float mx[NQ];
+    largest(s[0], mx);
+    follow(mx);
+    // Chunks 2 j and 2 j + 1 are stage j. Copies are requested two chunks before their first use: V of stage j + 1
+    // at chunk 2 j, K of stage j + 2 at chunk 2 j + 1. What is past the end is requested too (and nothing is read
+    // for it), so that the same number of copies is always on the way.
+    auto even = [&](unsigned char *kb, unsigned char *vb, unsigned char *vn, int from) __attribute__((always_inline)) {
+      landed(Count<kCopies>{});
+      copy(a.v, a.v_ld, vofs, vn, from + UNIT, keep1);
+      chunk(kb + kHalf, vb, s[0], s[1], (uint32_t)(keep >> 32));
+    };
+    auto odd = [&](unsigned char *kb, unsigned char *vb, unsigned char *kn, int from) __attribute__((always_inline)) {
+      landed(Count<kCopies>{});
+      keep = keep1;
+      keep1 = next_keep(from + 2 * UNIT);
+      copy(a.k, a.k_ld, kofs, kb, from + 2 * UNIT, keep1);
+      chunk(kn, vb + kHalf, s[1], s[0], (uint32_t)keep);
+    };
+    for (int from = first;; from += 2 * UNIT) {
+      even(k0, v0, v1, from);
+      if (from + 32 >= end) break;
+      odd(k0, v0, k1, from);
+      if (from + 64 >= end) break;
+      even(k1, v1, v0, from + UNIT);
+      if (from + 96 >= end) break;
+      odd(k1, v1, k0, from + UNIT);
+      if (from + 128 >= end) break;
+    }
+    landed(Count<0>{});  // what was requested past the end, before the stages are used again
+  }
+  if (r0 >= w.s.rows) return;
+  O::settle();
+  float *part = w.slot >= 0 ? slot_at<DP, BQ>(a, w.slot) : nullptr;
+  constants<NQ>([&](auto block) __attribute__((always_inline)) {
+    constexpr int i = decltype(block)::value;
     const int rt = wave * 32 * NQ + 32 * i + (lane & 31), r = w.tile * BQ + rt;
     const float l = st.l[i] + other_half(st.l[i]);
-    if (r >= w.s.rows) continue;
-    if (part) {
-#pragma unroll
-      for (int j = 0; j < DP / 32; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<f32x4 *>(part + ((int64_t)(8 * j + 2 * g + h) * BQ + rt) * 4) =
-              f32x4{st.o[i][j][4 * g], st.o[i][j][4 * g + 1], st.o[i][j][4 * g + 2], st.o[i][j][4 * g + 3]};
-      if (h == 0) {
-        part[(int64_t)BQ * DP + rt] = st.m[i];
-        part[(int64_t)BQ * (DP + 1) + rt] = l;
+    if (r >= w.s.rows) return;
+    const float f = reciprocal(l);
+    uint16_t *const o = out_row(a, w, r);
+    // four values of 8 g + 4 h on of each 32
+    constants<4 * kTiles>([&](auto four) __attribute__((always_inline)) {
+      constexpr int j = decltype(four)::value / 4, g = decltype(four)::value % 4;
+      const f32x4 v = O::template get<i * kTiles + j, 4 * g>();
+      if (part) {
+        *reinterpret_cast<f32x4 *>(part + ((int64_t)(8 * j + 2 * g + h) * BQ + rt) * 4) = v;
+      } else {
+        const int d = 32 * j + 8 * g + 4 * h;
+        if (d < a.D) *reinterpret_cast<u32x2 *>(o + d) = u32x2{pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f)};
       }
-    } else {
-      const float f = reciprocal(l);
-      uint16_t *o = out_row(a, w, r);
-#pragma unroll
-      for (int j = 0; j < DP / 32; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int d = 32 * j + 8 * g + 4 * h;
-          if (d < a.D)
-            *reinterpret_cast<u32x2 *>(o + d) = u32x2{pack_bf16(st.o[i][j][4 * g] * f, st.o[i][j][4 * g + 1] * f),
-                                                      pack_bf16(st.o[i][j][4 * g + 2] * f, st.o[i][j][4 * g + 3] * f)};
-        }
+    });
+    if (part && h == 0) {
+      part[(int64_t)BQ * DP + rt] = st.m[i];
+      part[(int64_t)BQ * (DP + 1) + rt] = l;
     }
-  }
+  });
 }
 
 // ------------------------------------------------------------------ tiles of few rows
@@ -472,14 +716,13 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
   using Div = Division<BQ, UNIT>;
   const Plan plan = Div::plan(a);
   Work w;
-  if ((int64_t)blockIdx.x < plan.whole) {
-    if (!Div::find(a, plan, blockIdx.x, 0, w)) return;
-  } else {
-    if (!Div::find(a, plan, -1, blockIdx.x - plan.whole, w)) return;
-  }
+  const bool is_whole = (int64_t)blockIdx.x < plan.whole;
+  if (!Div::find(a, plan, is_whole ? (int64_t)blockIdx.x : -1, (int64_t)blockIdx.x - plan.whole, w)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   State<DP, 1> st;
   load_q<DP, 1>(a, w, w.tile * BQ, st);
+#pragma unroll
+  for (int j = 0; j < DP / 32; ++j) st.o[0][j] = f32x16{};
   const float c = a.scale * 1.4426950408889634f;
   unsigned char *const kb = ks + wave * kBytes, *const vb = vs + wave * kBytes;
   // copy i of the wave: unit 64 i + lane of its tile
@@ -635,7 +878,7 @@ void launch_width(const AttentionArgs &a, const AttentionPlan &p, hipStream_t st
     if (a.slots) attention_join_kernel<DP, 32, 128><<<dim3((unsigned)p.cut, DP / 16), 64, 0, stream>>>(a);
   } else if (p.rows == 128) {
     launch_rows<DP, 1>(a, p, stream);
-  } else if constexpr (DP <= 128) {
+  } else {
     launch_rows<DP, 2>(a, p, stream);
   }
 }
@@ -646,7 +889,7 @@ AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, int q_head
   AttentionPlan p{};
   const int dp = padded(D);
   const int64_t rows = Mq * (q_heads / kv_heads), each = rows / std::max<int64_t>(samples, 1);
-  p.rows = each <= 32 ? 32 : each <= 128 || dp > 128 ? 128 : 256;
+  p.rows = each <= 32 ? 32 : each <= 128 ? 128 : 256;
   // tiles of all samples at most: whatever the offsets are, one more per sample than without them
   const int64_t tiles = ((rows + p.rows - 1) / p.rows + samples) * kv_heads;
   p.slots = workspace ? (p.rows == 32 ? 2 * kCus : kCus) : 0;

@@ -299,23 +299,63 @@ def test_bindings_take_device_tensors_only():
         ql.qlinear_qk_norm_rope(4, 64, q=q, q_out=q.clone())
 
 
-def test_mfma_operands_have_two_wait_states(tmp_path):
-    """The attention's products keep the wait states between a VALU write and an MFMA read (see test_isa_hazards)."""
+@pytest.fixture(scope="module")
+def assembly(tmp_path_factory):
+    """The attention's kernels as the library's flags compile them."""
     import os
     import subprocess
 
-    from test_isa_hazards import _hipcc, scan
+    from test_isa_hazards import _hipcc
 
     from group_wise_affine_qlinear_amd import build as qb
     if _hipcc() is None:
         pytest.skip("hipcc not available")
-    flags = [f for f in qb.source_flags("attention.hip") if f not in ("-fPIC", "-fvisibility=hidden")]
-    out = tmp_path / "attention.s"
+    flags = [f for f in qb.COMMON_FLAGS if f not in ("-fPIC", "-fvisibility=hidden")]
+    out = tmp_path_factory.mktemp("asm") / "attention.s"
     res = subprocess.run([_hipcc(), *flags, "--cuda-device-only", "-S", os.path.join(qb.CSRC, "attention.hip"), "-o", str(out)],
                          capture_output=True, text=True)
     assert res.returncode == 0, res.stderr[-2000:]
-    n, bad = scan(out.read_text())
+    return out.read_text()
+
+
+def test_mfma_operands_have_two_wait_states(assembly):
+    """The attention's products keep the wait states between a VALU write and an MFMA read (see test_isa_hazards)."""
+    from test_isa_hazards import scan
+    n, bad = scan(assembly)
     assert n > 0 and not bad, bad[:5]
+
+
+def test_accumulators_are_the_kernels_own(assembly):
+    """attention_kernel names its accumulators in instructions of its own: no instruction that the compiler made touches
+    an AGPR there, and no accumulator is read or written by them before the wait that a product needs."""
+    import re
+    kernels, name, own, since = 0, None, False, None
+    for raw in assembly.splitlines():
+        line = raw.split(";")[0].strip()
+        m = re.match(r"(_Z\w*attention_kernel\w*):", raw)
+        if m:
+            name, since = m.group(1), None
+            kernels += 1
+        elif raw.startswith(".Lfunc_end"):
+            name = None
+        if name is None:
+            continue
+        if "#ASMSTART" in raw or "#ASMEND" in raw:
+            own = "#ASMSTART" in raw
+            continue
+        if not line or line.startswith(".") or line.endswith(":"):
+            continue
+        agpr = re.search(r"\ba(\d+|\[)", line)
+        assert own or not agpr, (name, line)
+        op = line.split()[0]
+        # instructions since the last product of each block of straight code; s_nop n counts n + 1
+        if op.startswith("v_mfma") and agpr:
+            since = 0
+        elif op.startswith("v_accvgpr") and since is not None:
+            assert since >= 19, (name, line, since)
+        elif since is not None:
+            since += int(line.split()[1]) + 1 if op == "s_nop" else 1
+    assert kernels >= 12
 
 
 def test_host_code_under_asan_and_ubsan(tmp_path):
