@@ -55,154 +55,198 @@ __device__ __forceinline__ float other_half(float v) {
 
 // ------------------------------------------------------------------ which block does what
 
-// Rows, keys and tiles of one sample.
+// Rows and keys of one sample.
 struct Sample {
-  int64_t q0, k0;
+  int q0, k0;
   int rows, keys;  // rows: queries times the heads that share a key head
 };
 
 __device__ __forceinline__ Sample sample_of(const AttentionArgs &a, int s) {
-  Sample r = {0, 0, (int)(a.Mq * a.group), (int)a.Mk};
+  Sample r = {0, 0, (int)a.Mq * a.group, (int)a.Mk};
   if (a.q_offsets) {
     // whatever the offsets hold, no row outside the arrays is touched
-    const int64_t b = min(max((int64_t)a.q_offsets[s], (int64_t)0), a.Mq), e = min((int64_t)a.q_offsets[s + 1], a.Mq);
-    r.q0 = b;
-    r.rows = (int)(max(e - b, (int64_t)0) * a.group);
-  }
-  if (a.k_offsets) {
-    const int64_t b = min(max((int64_t)a.k_offsets[s], (int64_t)0), a.Mk), e = min((int64_t)a.k_offsets[s + 1], a.Mk);
-    r.k0 = b;
-    r.keys = (int)max(e - b, (int64_t)0);
+    const int Mq = (int)a.Mq, Mk = (int)a.Mk;
+    const auto within = [](int v, int most) { return min(max(v, 0), most); };
+    r.q0 = within(a.q_offsets[s], Mq);
+    r.k0 = within(a.k_offsets[s], Mk);
+    r.rows = max(within(a.q_offsets[s + 1], Mq) - r.q0, 0) * a.group;
+    r.keys = max(within(a.k_offsets[s + 1], Mk) - r.k0, 0);
   }
   return r;
 }
 
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
-  return (int64_t)((uint64_t)hi << 32 | lo);
-}
-
-// Inclusive sum over the 64 lanes.
-__device__ __forceinline__ int64_t scan(int64_t v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int64_t o = __shfl_up(v, d);
-    if ((int)(threadIdx.x & 63) >= d) v += o;
-  }
+// Sums over the lanes up to and with this one.
+template <typename T>
+__device__ __forceinline__ T scan(T v) {
+  auto add = [&](auto moved) { v += __builtin_bit_cast(T, moved); };
+  const auto bits = [&] { return __builtin_bit_cast(int, v); };
+  add(__builtin_amdgcn_update_dpp(0, bits(), 0x111, 0xF, 0xF, true));   // row_shr:1
+  add(__builtin_amdgcn_update_dpp(0, bits(), 0x112, 0xF, 0xF, true));   // row_shr:2
+  add(__builtin_amdgcn_update_dpp(0, bits(), 0x114, 0xF, 0xF, true));   // row_shr:4
+  add(__builtin_amdgcn_update_dpp(0, bits(), 0x118, 0xF, 0xF, true));   // row_shr:8
+  add(__builtin_amdgcn_update_dpp(0, bits(), 0x142, 0xA, 0xF, false));  // row_bcast:15 into rows 1 and 3
+  add(__builtin_amdgcn_update_dpp(0, bits(), 0x143, 0xC, 0xF, false));  // row_bcast:31 into rows 2 and 3
   return v;
 }
+template <typename T> __device__ __forceinline__ T lane_of(T v, int lane) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
 
-// The division of a call's tiles over blocks. The first `whole` tiles belong
-// to a block each; the keys of the others are cut into pieces of `per` units.
-// All of it follows from the offsets, so every block finds the same.
-struct Plan {
-  int64_t tiles, whole;
-  int per;
-};
+// A value that is the same in every lane, in a scalar register. The compiler
+// knows that of most of these, but has some in vector registers all the same
+// (loads that it cannot make scalar), and a buffer resource made of such a one
+// turns every copy into a loop over the lanes: so it is not told.
+__device__ __forceinline__ int uniform(int v) {
+  asm("" : "+v"(v));
+  return __builtin_amdgcn_readfirstlane(v);
+}
+__device__ __forceinline__ const uint16_t *uniform(const uint16_t *p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<const uint16_t *>((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
 
 struct Work {
   Sample s;
-  int head, tile;       // key head; tile of BQ rows
-  int unit0, unit1;     // units of keys
-  int64_t slot;         // where its partial sums go, -1: it writes the output
+  int head, tile;    // key head; tile of BQ rows
+  int unit0, unit1;  // units of keys
+  int slot;          // where its partial sums go (of a cut tile: the first piece's), -1: it writes the output
+  int parts;         // pieces of the tile
 };
+
+// A block's work in scalar registers. Where it is found it is one value of several branches, so each kernel asks for
+// this behind them.
+__device__ __forceinline__ Work uniform(const Work &w) {
+  return {{uniform(w.s.q0), uniform(w.s.k0), uniform(w.s.rows), uniform(w.s.keys)}, uniform(w.head), uniform(w.tile),
+          uniform(w.unit0), uniform(w.unit1), uniform(w.slot), uniform(w.parts)};
+}
+
+// The division of a call's tiles over blocks: which sample, head, rows and
+// keys a block has. The first `whole` tiles belong to a block each; the keys
+// of the others are cut into pieces of `per` units, so that about a.slots
+// pieces come out. All of it follows from the offsets, so every wave of every
+// block finds the same.
+constexpr int kMostBlocks = 1 << 24;  // of a call that is served
 
 template <int BQ, int UNIT>
 struct Division {
-  static __device__ __forceinline__ int64_t tiles_of(const AttentionArgs &a, const Sample &s) {
-    return (int64_t)((s.rows + BQ - 1) / BQ) * a.kv_heads;
+  const AttentionArgs &a;
+  Sample mine;  // the lane's of the first 64 samples
+  int tiles = 0, whole = 0, per = 1 << 30;
+
+  static __device__ __forceinline__ int tiles_of(const AttentionArgs &a, const Sample &s) {
+    return (s.rows + BQ - 1) / BQ * a.kv_heads;
   }
   static __device__ __forceinline__ int units_of(const Sample &s) { return max((s.keys + UNIT - 1) / UNIT, 1); }
 
-  // Calls f(sample index or -1, Sample) with 64 samples at a time, a lane each, until f returns true.
-  template <typename F>
-  static __device__ __forceinline__ void each(const AttentionArgs &a, F f) {
+  // Calls f(Sample, index of lane 0's) with 64 samples at a time, a lane each, until f returns true.
+  template <typename F> __device__ __forceinline__ void each(F f) {
     for (int s0 = 0; s0 < a.samples; s0 += 64) {
+      Sample x = mine;
       const int s = s0 + (int)(threadIdx.x & 63);
-      Sample x = {0, 0, 0, 0};
-      if (s < a.samples) x = sample_of(a, s);
-      if (f(s < a.samples ? s : -1, x)) return;
+      if (s0) x = s < a.samples ? sample_of(a, s) : Sample{0, 0, 0, 0};
+      if (f(x, s0)) return;
     }
   }
+  // Of a sample's n tiles, whose first is `begin`, those that are cut.
+  __device__ __forceinline__ int cut_of(int begin, int n) const { return min(max(begin + n - whole, 0), n); }
 
-  static __device__ __forceinline__ Plan plan(const AttentionArgs &a) {
-    Plan p = {0, 0, 1 << 30};
-    each(a, [&](int, const Sample &x) {
-      p.tiles += __shfl(scan(tiles_of(a, x)), 63);
-      return false;
-    });
-    p.tiles = uniform(p.tiles);
-    if (a.slots == 0) {
-      p.whole = p.tiles;
-      return p;
+  __device__ __forceinline__ explicit Division(const AttentionArgs &args) : a(args) {
+    if (a.samples == 1) {
+      mine = sample_of(a, 0);
+      tiles = tiles_of(a, mine);
+      whole = a.slots == 0 ? tiles : a.cut_all ? 0 : (int)((unsigned)tiles / (unsigned)a.slots) * a.slots;
+      // as many pieces of every tile as there are blocks for
+      const int cut = tiles - whole, most = cut > 0 ? max((int)((unsigned)a.slots / (unsigned)cut), 1) : 1;
+      if (cut > 0) per = max((units_of(mine) + most - 1) / most, a.least_units);
+      return;
     }
-    p.whole = a.cut_all ? 0 : p.tiles / a.slots * a.slots;
-    int64_t first = 0, units = 0;
-    each(a, [&](int, const Sample &x) {
-      const int64_t n = tiles_of(a, x), incl = scan(n);
-      const int64_t begin = first + incl - n, cut = min(max(begin + n - p.whole, (int64_t)0), n);
-      units += __shfl(scan(cut * units_of(x)), 63);
-      first += __shfl(incl, 63);
+    const int s = (int)(threadIdx.x & 63);
+    mine = s < a.samples ? sample_of(a, s) : Sample{0, 0, 0, 0};
+    each([&](const Sample &x, int) {
+      tiles = min(tiles + lane_of(scan(tiles_of(a, x)), 63), kMostBlocks);
       return false;
     });
-    p.per = (int)max((uniform(units) + a.slots - 1) / a.slots, (int64_t)a.least_units);
-    return p;
+    whole = a.slots == 0 ? tiles : a.cut_all ? 0 : (int)((unsigned)tiles / (unsigned)a.slots) * a.slots;
+    if (whole == tiles) return;
+    int first = 0;
+    float units = 0.f;  // counted to a few parts in a million
+    each([&](const Sample &x, int) {
+      const int n = tiles_of(a, x), incl = scan(n);
+      units += lane_of(scan((float)cut_of(first + incl - n, n) * (float)units_of(x)), 63);
+      first = min(first + lane_of(incl, 63), kMostBlocks);
+      return false;
+    });
+    // half a piece of every tile is empty on average
+    const int cut = tiles - whole;
+    per = max((int)min(units / (float)max(a.slots - cut / 2, a.slots / 2) + 1.f, 1e9f), a.least_units);
   }
 
-  // The tile `t` (of all, `t` >= 0), or the tile that the piece `b` of the cut ones belongs to (t < 0).
-  static __device__ __forceinline__ bool find(const AttentionArgs &a, const Plan &p, int64_t t, int64_t b, Work &w) {
-    int64_t first = 0, pieces = 0;
-    bool found = false;
-    // offsets that decrease may ask for more pieces than there is room for
-    if (t < 0 && b >= a.pieces) return false;
-    each(a, [&](int s, const Sample &x) {
-      const int64_t n = tiles_of(a, x), incl = scan(n);
-      const int64_t begin = first + incl - n;
-      const int64_t cut = min(max(begin + n - p.whole, (int64_t)0), n);  // the last `cut` tiles of the sample are cut
-      const int parts = (units_of(x) + p.per - 1) / p.per;
-      const int64_t pincl = scan(cut * parts), pbegin = pieces + pincl - cut * parts;
-      const bool mine = s >= 0 && (t >= 0 ? t >= begin && t < begin + n : b >= pbegin && b < pbegin + cut * parts);
-      const uint64_t who = __ballot(mine);
-      if (who) {
-        const int l = __builtin_ctzll(who);
-        const int sl = __shfl(s, l), np = __shfl(parts, l);
-        const int64_t nl = __shfl(n, l), cl = __shfl(cut, l), bl = __shfl(begin, l), pl = __shfl(pbegin, l);
-        w.s = sample_of(a, sl);
-        const int64_t in = t >= 0 ? t - bl : nl - cl + (b - pl) / np;
-        const int heads_tiles = (w.s.rows + BQ - 1) / BQ;
-        w.head = (int)(in / heads_tiles);
-        w.tile = (int)(in % heads_tiles);
-        const int all = units_of(w.s);
-        const bool is_cut = in >= nl - cl && np > 1;
-        const int piece = t >= 0 ? 0 : (int)((b - pl) % np);
-        w.unit0 = t >= 0 ? 0 : piece * p.per;
-        w.unit1 = t >= 0 ? all : min(all, w.unit0 + p.per);
-        // of a tile: the slot of its first piece
-        w.slot = is_cut ? (t >= 0 ? pl + (in - (nl - cl)) * np : b) : -1;
-        found = w.slot + (t >= 0 ? np : 1) <= a.pieces || !is_cut;
-        return true;
+  __device__ __forceinline__ void set(Work &w, int in, int piece, int parts) const {
+    const int row_tiles = (w.s.rows + BQ - 1) / BQ, units = units_of(w.s);
+    w.head = (unsigned)in / (unsigned)row_tiles;
+    w.tile = in - w.head * row_tiles;
+    w.parts = parts;
+    w.unit0 = parts > 1 ? piece * per : 0;
+    w.unit1 = parts > 1 ? min(units, w.unit0 + per) : units;
+  }
+
+  // What tile t (of all, t >= 0), or piece b of the cut ones (t < 0), is of; false if there is none.
+  // Of a tile all its pieces, with the first one's slot.
+  __device__ __forceinline__ bool find(int t, int b, Work &w) {
+    // offsets that decrease may ask for more tiles and pieces than there is room for
+    if (t < 0 && (b < 0 || b >= a.pieces)) return false;
+    if (a.samples == 1) {
+      w.s = mine;
+      const int parts = per < (1 << 30) ? (units_of(mine) + per - 1) / per : 1;
+      if (t >= 0) {
+        if (t >= tiles) return false;
+        set(w, t, 0, 1);
+        w.parts = t >= whole ? parts : 1;
+        w.slot = w.parts > 1 ? (t - whole) * parts : -1;
+      } else {
+        const int in = whole + (unsigned)b / (unsigned)parts;
+        if (in >= tiles) return false;
+        set(w, in, b - (in - whole) * parts, parts);
+        w.slot = parts > 1 ? b : -1;
       }
-      first += __shfl(incl, 63);
-      pieces += __shfl(pincl, 63);
-      return false;
-    });
-    // the same in every lane: addresses made of it stay scalar
-    w.s.q0 = uniform(w.s.q0);
-    w.s.k0 = uniform(w.s.k0);
-    w.s.rows = __builtin_amdgcn_readfirstlane(w.s.rows);
-    w.s.keys = __builtin_amdgcn_readfirstlane(w.s.keys);
-    w.head = __builtin_amdgcn_readfirstlane(w.head);
-    w.tile = __builtin_amdgcn_readfirstlane(w.tile);
-    w.unit0 = __builtin_amdgcn_readfirstlane(w.unit0);
-    w.unit1 = __builtin_amdgcn_readfirstlane(w.unit1);
-    w.slot = uniform(w.slot);
-    return __builtin_amdgcn_readfirstlane(found);
+    } else {
+      int first = 0, pieces = 0, found = 0;
+      each([&](const Sample &x, int s0) {
+        const int n = tiles_of(a, x), incl = scan(n), begin = first + incl - n;
+        const int cut = cut_of(begin, n), parts = (units_of(x) + per - 1) / per;
+        const int all = (int)min((int64_t)cut * parts, (int64_t)kMostBlocks);
+        const int pincl = scan(all), pbegin = pieces + pincl - all;
+        const uint64_t who = __ballot(t >= 0 ? t >= begin && t < begin + n : b >= pbegin && b < pbegin + all);
+        if (who) {
+          const int l = __builtin_ctzll(who);
+          const int nl = lane_of(n, l), cl = lane_of(cut, l), np = lane_of(parts, l), pl = lane_of(pbegin, l);
+          w.s = {lane_of(x.q0, l), lane_of(x.k0, l), lane_of(x.rows, l), lane_of(x.keys, l)};
+          if (t >= 0) {
+            const int in = t - lane_of(begin, l);
+            set(w, in, 0, 1);
+            w.parts = in >= nl - cl ? np : 1;
+            w.slot = w.parts > 1 ? pl + (in - (nl - cl)) * np : -1;
+          } else {
+            const int in = (unsigned)(b - pl) / (unsigned)np;
+            set(w, nl - cl + in, b - pl - in * np, np);
+            w.slot = np > 1 ? b : -1;
+          }
+          found = 1;
+          return true;
+        }
+        first = min(first + lane_of(incl, 63), kMostBlocks);
+        pieces = min(pieces + lane_of(pincl, 63), kMostBlocks);
+        return false;
+      });
+      if (!__builtin_amdgcn_readfirstlane(found)) return false;
+    }
+    return w.slot < 0 || w.slot + (t >= 0 ? w.parts : 1) <= a.pieces;
   }
 };
 
 // Consecutive logical blocks on one XCD, for any number of blocks.
-__device__ __forceinline__ int64_t xcd_order(int64_t b, int64_t n) {
-  const int64_t x = b & 7, each = n >> 3, more = n & 7;
+__device__ __forceinline__ int xcd_order(int b, int n) {
+  const int x = b & 7, each = n >> 3, more = n & 7;
   return x * each + min(x, more) + (b >> 3);
 }
 
@@ -222,22 +266,24 @@ struct State : Queries<DP, NQ> {
   f32x16 o[NQ][DP / 32];     // O^T
 };
 
+// Row r of a sample's rows: query r / group, head r % group of the key head's.
+__device__ __forceinline__ int query_of(const AttentionArgs &a, int r) { return a.group == 1 ? r : (unsigned)r / (unsigned)a.group; }
+
 // Query rows r0 + 32 i + (lane & 31) of a tile into registers; zeros past the rows and past D.
 template <int DP, int NQ>
 __device__ __forceinline__ void load_q(const AttentionArgs &a, const Work &w, int r0, Queries<DP, NQ> &st) {
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, m0 = query_of(a, r0);
+  const uint16_t *const p = a.q + (int64_t)(w.s.q0 + m0) * a.q_ld + (int64_t)w.head * a.group * a.D;
+  // 64 rows of a pitch of at most 2^22 values lie within the buffer
+  const auto rows = make_rsrc(uniform(p), 0, 0x7FFFFFFF);
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
-    const int r = r0 + 32 * i + (lane & 31);
-    const bool in = r < w.s.rows;
-    const int m = in ? r / a.group : 0, g = in ? r % a.group : 0;
-    const uint16_t *p = a.q + (w.s.q0 + m) * a.q_ld + (int64_t)(w.head * a.group + g) * a.D;
+    const int r = r0 + 32 * i + (lane & 31), m = query_of(a, r);
+    const int at = r < w.s.rows ? (int)((m - m0) * a.q_ld + (r - m * a.group) * a.D + 8 * (lane >> 5)) * 2 : kOut;
 #pragma unroll
     for (int j = 0; j < DP / 16; ++j) {
       const int d = 16 * j + 8 * (lane >> 5);
-      u32x4 v = {0, 0, 0, 0};
-      if (in && d < a.D) v = *reinterpret_cast<const u32x4 *>(p + d);
-      st.q[i][j] = as_bf16x8(v);
+      st.q[i][j] = as_bf16x8(__builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, d < a.D ? at + 32 * j : kOut, 0, 0)));
     }
     st.m[i] = kLowest;
     st.l[i] = 0.f;
@@ -337,15 +383,12 @@ __device__ __forceinline__ void outputs(const unsigned char *vb, int row0, State
     }
 }
 
-// Rows of K or V of one key head of a sample, from the sample's key `first` on.
+// Up to 64 rows of K or V of one key head of a sample, from the sample's key `first` on; what is past them reads as zeros.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const AttentionArgs &a, const uint16_t *x, int64_t ld,
                                                           const Work &w, int first) {
-  const int64_t rows = w.s.keys - first;
-  const uint16_t *p = x + (w.s.k0 + first) * ld + (int64_t)w.head * a.D;
-  // said to be the same in every lane here again: a resource that the compiler
-  // takes for the lanes' own makes every copy a loop over the lanes
-  return make_rsrc(reinterpret_cast<const void *>(uniform(reinterpret_cast<int64_t>(p))), 0,
-                   uniform(rows <= 0 ? 0 : ((rows - 1) * ld + a.D) * 2));
+  const int rows = min(w.s.keys - first, 64);
+  const uint16_t *p = x + (int64_t)(w.s.k0 + first) * ld + (int64_t)w.head * a.D;
+  return make_rsrc(p, 0, rows <= 0 ? 0 : ((rows - 1) * (int)ld + a.D) * 2);
 }
 
 // Bits of the keys [first, first + 64) of the sample that are kept.
@@ -358,16 +401,17 @@ __device__ __forceinline__ uint64_t kept(const AttentionArgs &a, const Work &w, 
 }
 __device__ __forceinline__ int mask_byte(const AttentionArgs &a, const Work &w, int first) {
   const int j = first + (int)(threadIdx.x & 63);
-  return j < w.s.keys ? a.key_mask[w.s.k0 + j] : 0;
+  return j < w.s.keys ? a.key_mask[(int64_t)w.s.k0 + j] : 0;
 }
 
 // Partial sums of a tile: [DP / 4][rows][4] outputs, then the maxima, then the sums, fp32.
-template <int DP, int BQ> __device__ __forceinline__ float *slot_at(const AttentionArgs &a, int64_t slot) {
+template <int DP, int BQ> __device__ __forceinline__ float *slot_at(const AttentionArgs &a, int slot) {
   return a.partial + slot * (int64_t)(BQ * (DP + 2));
 }
 
 __device__ __forceinline__ uint16_t *out_row(const AttentionArgs &a, const Work &w, int r) {
-  return a.out + (w.s.q0 + r / a.group) * a.out_ld + (int64_t)(w.head * a.group + r % a.group) * a.D;
+  const int m = query_of(a, r);
+  return a.out + (int64_t)(w.s.q0 + m) * a.out_ld + (int64_t)(w.head * a.group + r - m * a.group) * a.D;
 }
 
 // Sum over both halves, 1 / it, or 0 where there is no weight at all.
@@ -489,18 +533,18 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
   constexpr int kCopies = UNIT * kUnits / 256;  // copies of 64 units per wave and stage
   constexpr int kSteps = DP / 16, kFrags = DP / 16;
   __shared__ __attribute__((aligned(16))) unsigned char k0[kBytes], k1[kBytes], v0[kBytes], v1[kBytes];
-  using Div = Division<BQ, UNIT>;
-  const Plan plan = Div::plan(a);
+  Division<BQ, UNIT> division(a);
   Work w;
-  const bool is_whole = (int64_t)blockIdx.x < plan.whole;
-  if (!Div::find(a, plan, is_whole ? xcd_order(blockIdx.x, plan.whole) : -1, (int64_t)blockIdx.x - plan.whole, w)) return;
+  const int block = blockIdx.x, whole = division.whole;
+  if (!division.find(block < whole ? xcd_order(block, whole) : -1, block - whole, w)) return;
+  w = uniform(w);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, h = lane >> 5;
   const int r0 = w.tile * BQ + wave * 32 * NQ;
   using O = Acc<NQ * DP / 32>;
   constexpr int kTiles = DP / 32;  // of a query block
   Queries<DP, NQ> st;
   load_q<DP, NQ>(a, w, r0, st);
-  const float c = a.scale * 1.4426950408889634f;
+  const float c = __uint_as_float(uniform((int)__float_as_uint(a.scale * 1.4426950408889634f)));
   const Lanes<DP> at;
 
   // copy i of this wave: unit (4 i + wave) * 64 + lane of the stage
@@ -510,14 +554,26 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
   const int kofs = kc * 8 < a.D ? (int)(row * a.k_ld + kc * 8) * 2 : kOut;
   const int vofs = vc * 8 < a.D ? (int)(row * a.v_ld + vc * 8) * 2 : kOut;
   const int first = w.unit0 * UNIT, end = min(w.unit1 * UNIT, w.s.keys);
-  auto copy = [&](const uint16_t *x, int64_t ld, int ofs, unsigned char *to, int from, uint64_t keep) __attribute__((always_inline)) {
-    const auto r = rows_of(a, x, ld, w, from);
-    const uint32_t step = (uint32_t)(kRows * ld * 2);
-    uint32_t o = ofs;
-    asm volatile("" : "+v"(o));  // or every copy's offset is kept in a register over the loop
+  // The copies of one stage of K or V, requested one at a time.
+  struct Copies {
+    __amdgpu_buffer_rsrc_t rows;
+    uint32_t ofs, step;
+    unsigned char *to;
+    uint64_t keep;
+    int row;
+    __device__ __forceinline__ void one(int i) {
+      dma16(rows, !MASKED || (keep >> (row + i * kRows) & 1) ? ofs : kOut, 0, to + i * 4096);
+      ofs += step;
+    }
+    __device__ __forceinline__ void all() {
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i)
-      dma16(r, !MASKED || (keep >> (row + i * kRows) & 1) ? o + i * step : kOut, 0, to + (4 * i + wave) * 1024);
+      for (int i = 0; i < kCopies; ++i) one(i);
+    }
+  };
+  auto copies = [&](const uint16_t *x, int64_t ld, int ofs, unsigned char *to, int from, uint64_t keep) __attribute__((always_inline)) {
+    Copies c = {rows_of(a, x, ld, w, from), (uint32_t)ofs, (uint32_t)(kRows * ld * 2), to + wave * 1024, keep, row};
+    asm volatile("" : "+v"(c.ofs));  // or every copy's offset is kept in a register over the loop
+    return c;
   };
   // Kept keys of the stages in hand; a stage's bytes of the mask are requested two stages ahead.
   uint64_t keep = 0, keep1 = 0;
@@ -578,17 +634,25 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
   };
 
   // One chunk: its scores `x` meet V's rows at vb; meanwhile the next chunk's
-  // become y (K rows at kb, kept keys `valid`).
-  auto chunk = [&](const unsigned char *kb, const unsigned char *vb, f32x16 (&x)[NQ], f32x16 (&y)[NQ], uint32_t valid) __attribute__((always_inline)) {
+  // become y (K rows at kb, kept keys `valid`) and `c2` is requested. An MFMA
+  // keeps the matrix unit for 32 cycles: after each one goes what the vector
+  // unit can do meanwhile, in this order and no other.
+  auto chunk = [&](const unsigned char *kb, const unsigned char *vb, f32x16 (&x)[NQ], f32x16 (&y)[NQ], uint32_t valid, Copies c2)
+      __attribute__((always_inline)) {
     uint32_t p[NQ][8];
-    constexpr int kPairs = NQ * 8;
-    auto pair = [&](int e) __attribute__((always_inline)) {  // weights 2 (e % 8) and the next of query block e / 8
-      const int i = e / 8, r = e % 8 * 2;
-      p[i][r / 2] = pack_bf16(__builtin_amdgcn_exp2f(__builtin_fmaf(x[i][r], c, -st.m[i])),
-                              __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][r + 1], c, -st.m[i])));
-      const bf16x2 one = {(__bf16)1.f, (__bf16)1.f};
-      st.l[i] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p[i][r / 2]), one, st.l[i], false);
-      asm volatile("" : "+v"(p[i][r / 2]), "+v"(st.l[i]));  // stays between the MFMAs where it is placed
+    float e0 = 0.f, e1 = 0.f;
+    // half n of the 16 NQ: the exponents and the first power of two weights, then the second and their sum
+    auto half = [&](int n) __attribute__((always_inline)) {
+      const int i = n / 16, r = n % 16 / 2 * 2;
+      if (n % 2 == 0) {
+        e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][r], c, -st.m[i]));
+        e1 = __builtin_fmaf(x[i][r + 1], c, -st.m[i]);
+      } else {
+        p[i][r / 2] = pack_bf16(e0, __builtin_amdgcn_exp2f(e1));
+        const bf16x2 one = {(__bf16)1.f, (__bf16)1.f};
+        st.l[i] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p[i][r / 2]), one, st.l[i], false);
+        asm volatile("" : "+v"(p[i][r / 2]), "+v"(st.l[i]));
+      }
     };
     bf16x8 kf[3];
     kf[0] = at.k_frag(kb, 0);
@@ -597,13 +661,15 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
     for (int i = 0; i < NQ; ++i) y[i] = f32x16{};
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      if (j + 2 < kSteps) kf[(j + 2) % 3] = at.k_frag(kb, j + 2);
+    for (int n = 0; n < kSteps * NQ; ++n) {
+      const int j = n / NQ, i = n % NQ;
+      if (i == 0 && j + 2 < kSteps) kf[(j + 2) % 3] = at.k_frag(kb, j + 2);
+      y[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[j % 3], st.q[i][j], y[i], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) y[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[j % 3], st.q[i][j], y[i], 0, 0, 0);
-#pragma unroll
-      for (int u = 0; u < (kPairs + kSteps - 1) / kSteps; ++u)
-        if (j * kPairs / kSteps + u < (j + 1) * kPairs / kSteps) pair(j * kPairs / kSteps + u);
+      for (int u = 0; u < (16 + kSteps - 1) / kSteps; ++u)
+        if (n * 16 / kSteps + u < (n + 1) * 16 / kSteps) half(n * 16 / kSteps + u);
+      if (i == NQ - 1 && j * kCopies / kSteps < (j + 1) * kCopies / kSteps) c2.one(j * kCopies / kSteps);
       __builtin_amdgcn_sched_barrier(0);
     }
     hide(y, valid);
@@ -612,16 +678,13 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
     vf[1] = at.v_frag(vb, 1);
     float mx[NQ];
     __builtin_amdgcn_sched_barrier(0);
-    constants<kFrags>([&](auto count) __attribute__((always_inline)) {
-      constexpr int f = decltype(count)::value, t = f / kTiles, j = f % kTiles;
-      if constexpr (f + 2 < kFrags) vf[(f + 2) % 3] = at.v_frag(vb, f + 2);
-      O::template mfma<j>(vf[f % 3], as_bf16x8(u32x4{p[0][4 * t], p[0][4 * t + 1], p[0][4 * t + 2], p[0][4 * t + 3]}));
-      if constexpr (NQ == 2)
-        O::template mfma<kTiles + j>(vf[f % 3], as_bf16x8(u32x4{p[1][4 * t], p[1][4 * t + 1], p[1][4 * t + 2], p[1][4 * t + 3]}));
+    constants<kFrags * NQ>([&](auto count) __attribute__((always_inline)) {
+      constexpr int n = decltype(count)::value, f = n / NQ, i = n % NQ, t = f / kTiles, j = f % kTiles;
+      if constexpr (i == 0 && f + 2 < kFrags) vf[(f + 2) % 3] = at.v_frag(vb, f + 2);
+      O::template mfma<i * kTiles + j>(vf[f % 3], as_bf16x8(u32x4{p[i][4 * t], p[i][4 * t + 1], p[i][4 * t + 2], p[i][4 * t + 3]}));
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int r = f * 16 / kFrags; r < (f + 1) * 16 / kFrags; ++r)
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) mx[i] = r ? fmaxf(mx[i], y[i][r]) : y[i][0];
+      for (int r = f * 16 / kFrags; r < (f + 1) * 16 / kFrags; ++r) mx[i] = r ? fmaxf(mx[i], y[i][r]) : y[i][0];
       __builtin_amdgcn_sched_barrier(0);
     });
     follow(mx);
@@ -638,9 +701,9 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
     if constexpr (MASKED) byte = mask_byte(a, w, first);
     keep = next_keep(first);
     keep1 = next_keep(first + UNIT);
-    copy(a.k, a.k_ld, kofs, k0, first, keep);
-    copy(a.v, a.v_ld, vofs, v0, first, keep);
-    copy(a.k, a.k_ld, kofs, k1, first + UNIT, keep1);
+    copies(a.k, a.k_ld, kofs, k0, first, keep).all();
+    copies(a.v, a.v_ld, vofs, v0, first, keep).all();
+    copies(a.k, a.k_ld, kofs, k1, first + UNIT, keep1).all();
     __builtin_amdgcn_s_waitcnt(((2 * kCopies) & 0xF) | (((2 * kCopies) >> 4) << 14) | 0xF70);
     __syncthreads();
     scores_of(k0, s[0]);
@@ -653,15 +716,13 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
     // for it), so that the same number of copies is always on the way.
     auto even = [&](unsigned char *kb, unsigned char *vb, unsigned char *vn, int from) __attribute__((always_inline)) {
       landed(Count<kCopies>{});
-      copy(a.v, a.v_ld, vofs, vn, from + UNIT, keep1);
-      chunk(kb + kHalf, vb, s[0], s[1], (uint32_t)(keep >> 32));
+      chunk(kb + kHalf, vb, s[0], s[1], (uint32_t)(keep >> 32), copies(a.v, a.v_ld, vofs, vn, from + UNIT, keep1));
     };
     auto odd = [&](unsigned char *kb, unsigned char *vb, unsigned char *kn, int from) __attribute__((always_inline)) {
       landed(Count<kCopies>{});
       keep = keep1;
       keep1 = next_keep(from + 2 * UNIT);
-      copy(a.k, a.k_ld, kofs, kb, from + 2 * UNIT, keep1);
-      chunk(kn, vb + kHalf, s[1], s[0], (uint32_t)keep);
+      chunk(kn, vb + kHalf, s[1], s[0], (uint32_t)keep, copies(a.k, a.k_ld, kofs, kb, from + 2 * UNIT, keep1));
     };
     for (int from = first;; from += 2 * UNIT) {
       even(k0, v0, v1, from);
@@ -713,17 +774,17 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
   constexpr int BQ = 32, UNIT = 128, kBytes = 32 * DP * 2, kUnits = DP / 8, kCopies = 32 * kUnits / 64;
   __shared__ __attribute__((aligned(16))) unsigned char ks[4 * kBytes], vs[4 * kBytes];
   __shared__ float ms[4][32], ls[4][32];
-  using Div = Division<BQ, UNIT>;
-  const Plan plan = Div::plan(a);
+  Division<BQ, UNIT> division(a);
   Work w;
-  const bool is_whole = (int64_t)blockIdx.x < plan.whole;
-  if (!Div::find(a, plan, is_whole ? (int64_t)blockIdx.x : -1, (int64_t)blockIdx.x - plan.whole, w)) return;
+  const int block = blockIdx.x, whole = division.whole;
+  if (!division.find(block < whole ? block : -1, block - whole, w)) return;
+  w = uniform(w);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   State<DP, 1> st;
   load_q<DP, 1>(a, w, w.tile * BQ, st);
 #pragma unroll
   for (int j = 0; j < DP / 32; ++j) st.o[0][j] = f32x16{};
-  const float c = a.scale * 1.4426950408889634f;
+  const float c = __uint_as_float(uniform((int)__float_as_uint(a.scale * 1.4426950408889634f)));
   unsigned char *const kb = ks + wave * kBytes, *const vb = vs + wave * kBytes;
   // copy i of the wave: unit 64 i + lane of its tile
   auto copy = [&](const uint16_t *x, int64_t ld, bool is_k, unsigned char *to, int at, uint32_t keep) {
@@ -822,13 +883,13 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
 // 16 values; a thread has one row.
 template <int DP, int BQ, int UNIT>
 __global__ __launch_bounds__(BQ < 64 ? 64 : BQ) void attention_join_kernel(AttentionArgs a) {
-  using Div = Division<BQ, UNIT>;
-  const Plan plan = Div::plan(a);
+  Division<BQ, UNIT> division(a);
   Work w;
-  if (plan.whole + (int64_t)blockIdx.x >= plan.tiles || !Div::find(a, plan, plan.whole + blockIdx.x, 0, w) || w.slot < 0) return;
+  if (!division.find(division.whole + (int)blockIdx.x, 0, w) || w.slot < 0) return;
+  w = uniform(w);
   const int rt = threadIdx.x % BQ, r = w.tile * BQ + rt;
   if (r >= w.s.rows) return;
-  const int pieces = (w.unit1 + plan.per - 1) / plan.per;
+  const int pieces = w.parts;
   const float *part = slot_at<DP, BQ>(a, w.slot);
   constexpr int64_t kSlot = BQ * (DP + 2);
   float m = kLowest, sum = 0.f;
