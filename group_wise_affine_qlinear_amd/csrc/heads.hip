@@ -12,8 +12,8 @@
 // A head lies on the power of two of lanes that holds 8 values each, so a
 // wave works on 64 / lanes heads at once, every value is read once and written
 // once and the sums of a norm are DPP moves. The angles depend on the row
-// alone: a wave makes its lanes' four cosines and sines once per row and turns
-// all of its heads by them.
+// alone: the threads of a block make each cosine and sine of its rows once and
+// all heads are turned by them from LDS.
 #include "ql_block.h"
 #include "ql_kernels.h"
 
@@ -137,105 +137,116 @@ __device__ __forceinline__ void normalise(float (&v)[8], int kind, float eps, fl
   }
 }
 
+constexpr int kPairs = 128;  // of a head of 256
+
 // Grid: x rows, y ranges of a row's steps; a step is the 64 >> lg heads that a
 // wave holds at once, the steps of q first, then k's, then v's.
 template <typename T, bool PAIRS, bool VEC>
 __global__ __launch_bounds__(256) void qk_norm_rope_kernel(HeadsArgs a) {
+  __shared__ __attribute__((aligned(16))) float turn[kPairs][2];  // cosine and sine
   const int64_t m = blockIdx.x;
   if (a.rows_end && m >= *a.rows_end) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lg = a.lane_bits, slot = lane & ((1 << lg) - 1), sub = lane >> lg, per = 64 >> lg;
   const bool live = slot * 8 < a.D;
-  const int turning = a.pairs / 4;  // slots that hold turned pairs
-  const bool turns = slot < turning;
+  const bool turns = slot < a.pairs / 4;  // the slot holds turned pairs
   const int lo = !PAIRS && turns ? slot * 4 : slot * 8;
   const int hi = !PAIRS && turns ? a.pairs + slot * 4 : slot * 8 + 4;
 
   const int steps_q = (a.part[0].heads + per - 1) / per, steps_k = (a.part[1].heads + per - 1) / per;
   const int steps = steps_q + steps_k + (a.part[2].heads + per - 1) / per;
   const int stride = 4 * gridDim.y;
-  // the part, first head and address of step i; the address only where the lane has a head of it
+  // the part and head of step i; whether the lane has a value of it
   auto where = [&](int i, int &p, int64_t &head) {
     p = i < steps_q ? 0 : i < steps_q + steps_k ? 1 : 2;
     head = (int64_t)(i - (p == 0 ? 0 : p == 1 ? steps_q : steps_q + steps_k)) * per + sub;
     return live && i < steps && head < a.part[p].heads;
   };
-  Piece<T, VEC> next = {};
   int i = blockIdx.y * 4 + wave;
-  {
+  // two steps are on their way at any time, the first two while the angles are made
+  Piece<T, VEC> next[2] = {};
+  auto load = [&](int i, Piece<T, VEC> &to) {
     int p;
     int64_t head;
-    if (where(i, p, head)) next.load(a.part[p].in, m * a.part[p].in_ld + head * a.D, lo, hi);
-  }
-
-  // angles in turns, in 64 bits: what is left of a far position's angle after
-  // whole turns is then as exact as a near one's
-  float cs[4], sn[4];
-  if (turning > 0 && i < steps_q + steps_k) {
+    if (where(i, p, head)) to.load(a.part[p].in, m * a.part[p].in_ld + head * a.D, lo, hi);
+  };
+  load(i, next[0]);
+  load(i + stride, next[1]);
+  // weights of q and k
+  float w[2][8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      cs[e] = 1.f;
-      sn[e] = 0.f;
-      if (turns) {
-        const int pair = slot * 4 + e;
-        const int axis = a.pair_axis ? a.pair_axis[pair] : 0;
-        if ((unsigned)axis < (unsigned)a.axes) {
-          double t = (double)a.positions[axis * a.M + m] * ((double)a.freqs[pair] * 0.15915494309189533577);
-          t -= rint(t);
-          sincospif(2.f * (float)t, &sn[e], &cs[e]);
-        }
-      }
+  for (int p = 0; p < 2; ++p) {
+    if (a.part[p].weight && live) {
+      Piece<F32, VEC> weight;
+      weight.load(a.part[p].weight, 0, lo, hi);
+      weight.values(w[p]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[p][e] = 1.f;
     }
   }
 
-  float w[8];
-  int held = -1;  // part whose weights are in w
+  if (a.pairs > 0) {
+    if ((int)threadIdx.x < a.pairs) {
+      const int pair = threadIdx.x, axis = a.pair_axis ? a.pair_axis[pair] : 0;
+      float cs = 1.f, sn = 0.f;
+      if ((unsigned)axis < (unsigned)a.axes) {
+        // in turns, in 64 bits: what is left of a far position's angle after
+        // whole turns is then as exact as a near one's
+        double x = (double)a.positions[axis * a.M + m] * ((double)a.freqs[pair] * 0.15915494309189533577);
+        x -= rint(x);
+        sincospif(2.f * (float)x, &sn, &cs);
+      }
+      turn[pair][0] = cs;
+      turn[pair][1] = sn;
+    }
+    __syncthreads();
+  }
+
   const float inv_d = 1.f / (float)a.D;
-  for (; i < steps; i += stride) {
+  auto step = [&](Piece<T, VEC> &piece) __attribute__((always_inline)) {
     int p;
     int64_t head;
     const bool here = where(i, p, head);
     float v[8];
-    next.values(v);
-    {
-      int pn;
-      int64_t hn;
-      if (where(i + stride, pn, hn)) next.load(a.part[pn].in, m * a.part[pn].in_ld + hn * a.D, lo, hi);
-    }
+    piece.values(v);
+    load(i + 2 * stride, piece);
     if (p != 2) {
       if (!here) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 0.f;
       }
       if (a.norm) normalise(v, a.norm, a.eps, inv_d, lg, live);
-      if (a.part[p].weight) {
-        if (held != p) {
-          held = p;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = live ? a.part[p].weight[(e < 4 ? lo : hi - 4) + e] : 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= w[e];
-      }
+      for (int e = 0; e < 8; ++e) v[e] *= p == 0 ? w[0][e] : w[1][e];
       if (turns) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
+          const float cs = turn[slot * 4 + e][0], sn = turn[slot * 4 + e][1];
           float &x = v[PAIRS ? 2 * e : e], &y = v[PAIRS ? 2 * e + 1 : e + 4];
           const float x0 = x, y0 = y;
-          x = __builtin_fmaf(x0, cs[e], -(y0 * sn[e]));
-          y = __builtin_fmaf(y0, cs[e], x0 * sn[e]);
+          x = __builtin_fmaf(x0, cs, -(y0 * sn));
+          y = __builtin_fmaf(y0, cs, x0 * sn);
         }
       }
     }
     if (here) store<VEC>(a.part[p].out, m * a.part[p].out_ld + head * a.D, lo, hi, v);
+  };
+  for (; i < steps; i += stride) {
+    step(next[0]);
+    i += stride;
+    if (i >= steps) break;
+    step(next[1]);
   }
 }
 
 }  // namespace
 
 hipError_t launch_qk_norm_rope(const HeadsArgs &a, hipStream_t stream) {
-  // Few rows leave CUs idle: their steps are then divided over up to as many
-  // blocks as keep 512 in all, each of which makes the row's angles again.
+  // One row to a block: 5.4 TB/s at 16896 rows of 54 heads of 256, where two
+  // rows, half a row or a quarter give 5.1, 5.1 and 4.7. Few rows would leave
+  // CUs idle: their steps are divided over up to as many blocks as keep 512 in
+  // all, each of which makes the row's angles again.
   const int per = 64 >> a.lane_bits;
   int steps = 0;
   for (const auto &p : a.part) steps += (p.heads + per - 1) / per;

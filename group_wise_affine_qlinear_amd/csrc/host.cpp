@@ -1078,7 +1078,8 @@ QL_API int qlinear_qk_norm_rope(const ql_qk_args *a, void *stream) {
     if (!p.in) continue;
     if (p.in_ld < p.heads * D || p.out_ld < p.heads * D) return QL_EINVAL;
     if (p.in == p.out && (p.in_ld != p.out_ld || a->in_dtype != QL_OUT_BF16)) return QL_EINVAL;
-    vec = vec && on_elements(p.in, 4 * in_bytes) && on_elements(p.out, 8) && p.in_ld % 4 == 0 && p.out_ld % 4 == 0;
+    vec = vec && on_elements(p.in, 4 * in_bytes) && on_elements(p.out, 8) && aligned16(p.weight) && p.in_ld % 4 == 0 &&
+          p.out_ld % 4 == 0;
     k.part[i] = {p.in, static_cast<uint16_t *>(p.out), p.in_ld, p.out_ld, p.weight, (int)p.heads};
   }
   for (const auto &p : parts)
