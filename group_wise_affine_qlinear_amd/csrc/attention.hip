@@ -543,7 +543,6 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
   using O = Acc<NQ * DP / 32>;
   constexpr int kTiles = DP / 32;  // of a query block
   Queries<DP, NQ> st;
-  load_q<DP, NQ>(a, w, r0, st);
   const float c = __uint_as_float(uniform((int)__float_as_uint(a.scale * 1.4426950408889634f)));
   const Lanes<DP> at;
 
@@ -696,14 +695,15 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
     __syncthreads();
   };
 
-  O::clear();
   if (first < end) {
     if constexpr (MASKED) byte = mask_byte(a, w, first);
     keep = next_keep(first);
     keep1 = next_keep(first + UNIT);
     copies(a.k, a.k_ld, kofs, k0, first, keep).all();
+    load_q<DP, NQ>(a, w, r0, st);
     copies(a.v, a.v_ld, vofs, v0, first, keep).all();
     copies(a.k, a.k_ld, kofs, k1, first + UNIT, keep1).all();
+    O::clear();
     __builtin_amdgcn_s_waitcnt(((2 * kCopies) & 0xF) | (((2 * kCopies) >> 4) << 14) | 0xF70);
     __syncthreads();
     scores_of(k0, s[0]);
@@ -735,33 +735,52 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
       if (from + 128 >= end) break;
     }
     landed(Count<0>{});  // what was requested past the end, before the stages are used again
+  } else {
+    O::clear();
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) st.m[i] = kLowest, st.l[i] = 0.f;
   }
   if (r0 >= w.s.rows) return;
   O::settle();
-  float *part = w.slot >= 0 ? slot_at<DP, BQ>(a, w.slot) : nullptr;
+  if (w.slot >= 0) {
+    float *const part = slot_at<DP, BQ>(a, w.slot);
+    constants<NQ>([&](auto block) __attribute__((always_inline)) {
+      constexpr int i = decltype(block)::value;
+      const int rt = wave * 32 * NQ + 32 * i + (lane & 31);
+      const float l = st.l[i] + other_half(st.l[i]);
+      // four values of 8 g + 4 h on of each 32: of the 32 queries side by side
+      constants<4 * kTiles>([&](auto four) __attribute__((always_inline)) {
+        constexpr int j = decltype(four)::value / 4, g = decltype(four)::value % 4;
+        *reinterpret_cast<f32x4 *>(part + ((8 * j + 2 * g + h) * BQ + rt) * 4) = O::template get<i * kTiles + j, 4 * g>();
+      });
+      if (h == 0) {
+        part[BQ * DP + rt] = st.m[i];
+        part[BQ * (DP + 1) + rt] = l;
+      }
+    });
+    return;
+  }
+  // Whole rows leave through the wave's quarter of LDS (a lane holds every
+  // eighth four values of a row: stored as they are, a call of 512 keys spends
+  // a fifth of its time on it). Units of 16 bytes are moved by the row.
+  unsigned char *const rows = wave == 0 ? k0 : wave == 1 ? k1 : wave == 2 ? v0 : v1;
   constants<NQ>([&](auto block) __attribute__((always_inline)) {
     constexpr int i = decltype(block)::value;
-    const int rt = wave * 32 * NQ + 32 * i + (lane & 31), r = w.tile * BQ + rt;
-    const float l = st.l[i] + other_half(st.l[i]);
-    if (r >= w.s.rows) return;
-    const float f = reciprocal(l);
-    uint16_t *const o = out_row(a, w, r);
-    // four values of 8 g + 4 h on of each 32
+    const float f = reciprocal(st.l[i] + other_half(st.l[i]));
+    const int q = 32 * i + (lane & 31);
     constants<4 * kTiles>([&](auto four) __attribute__((always_inline)) {
       constexpr int j = decltype(four)::value / 4, g = decltype(four)::value % 4;
       const f32x4 v = O::template get<i * kTiles + j, 4 * g>();
-      if (part) {
-        *reinterpret_cast<f32x4 *>(part + ((int64_t)(8 * j + 2 * g + h) * BQ + rt) * 4) = v;
-      } else {
-        const int d = 32 * j + 8 * g + 4 * h;
-        if (d < a.D) *reinterpret_cast<u32x2 *>(o + d) = u32x2{pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f)};
-      }
+      *reinterpret_cast<u32x2 *>(rows + q * (DP * 2) + (((4 * j + g) ^ q) & (kUnits - 1)) * 16 + h * 8) =
+          u32x2{pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f)};
     });
-    if (part && h == 0) {
-      part[(int64_t)BQ * DP + rt] = st.m[i];
-      part[(int64_t)BQ * (DP + 1) + rt] = l;
-    }
   });
+#pragma unroll 4
+  for (int n = 0; n < 32 * NQ * kUnits / 64; ++n) {
+    const int q = n * (64 / kUnits) + lane / kUnits, u = lane % kUnits;
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(rows + q * (DP * 2) + ((u ^ q) & (kUnits - 1)) * 16);
+    if (r0 + q < w.s.rows && u * 8 < a.D) *reinterpret_cast<u32x4 *>(out_row(a, w, r0 + q) + u * 8) = v;
+  }
 }
 
 // ------------------------------------------------------------------ tiles of few rows
