@@ -147,6 +147,11 @@ struct Division {
       if (f(x, s0)) return;
     }
   }
+  // Pieces of a cut tile.
+  __device__ __forceinline__ int parts_of(const Sample &s) const {
+    const int units = units_of(s);
+    return units < a.cut_units ? 1 : (units + per - 1) / per;
+  }
   // Of a sample's n tiles, whose first is `begin`, those that are cut.
   __device__ __forceinline__ int cut_of(int begin, int n) const { return min(max(begin + n - whole, 0), n); }
 
@@ -156,8 +161,11 @@ struct Division {
       tiles = tiles_of(a, mine);
       whole = a.slots == 0 ? tiles : a.cut_all ? 0 : (int)((unsigned)tiles / (unsigned)a.slots) * a.slots;
       // as many pieces of every tile as there are blocks for
-      const int cut = tiles - whole, most = cut > 0 ? max((int)((unsigned)a.slots / (unsigned)cut), 1) : 1;
-      if (cut > 0) per = max((units_of(mine) + most - 1) / most, a.least_units);
+      const int cut = tiles - whole, units = units_of(mine);
+      if (cut > 0) {
+        const int most = max(min((int)((unsigned)a.slots / (unsigned)cut), units / a.least_units), 1);
+        per = (units + most - 1) / most;
+      }
       return;
     }
     const int s = (int)(threadIdx.x & 63);
@@ -197,7 +205,7 @@ struct Division {
     if (t < 0 && (b < 0 || b >= a.pieces)) return false;
     if (a.samples == 1) {
       w.s = mine;
-      const int parts = per < (1 << 30) ? (units_of(mine) + per - 1) / per : 1;
+      const int parts = parts_of(mine);
       if (t >= 0) {
         if (t >= tiles) return false;
         set(w, t, 0, 1);
@@ -213,7 +221,7 @@ struct Division {
       int first = 0, pieces = 0, found = 0;
       each([&](const Sample &x, int s0) {
         const int n = tiles_of(a, x), incl = scan(n), begin = first + incl - n;
-        const int cut = cut_of(begin, n), parts = (units_of(x) + per - 1) / per;
+        const int cut = cut_of(begin, n), parts = parts_of(x);
         const int all = (int)min((int64_t)cut * parts, (int64_t)kMostBlocks);
         const int pincl = scan(all), pbegin = pieces + pincl - all;
         const uint64_t who = __ballot(t >= 0 ? t >= begin && t < begin + n : b >= pbegin && b < pbegin + all);
@@ -535,7 +543,7 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
   __shared__ __attribute__((aligned(16))) unsigned char k0[kBytes], k1[kBytes], v0[kBytes], v1[kBytes];
   Division<BQ, UNIT> division(a);
   Work w;
-  const int block = blockIdx.x, whole = division.whole;
+  const int block = blockIdx.x, whole = a.rest_from ? a.rest_from : division.whole;
   if (!division.find(block < whole ? xcd_order(block, whole) : -1, block - whole, w)) return;
   w = uniform(w);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, h = lane >> 5;
@@ -787,22 +795,30 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
 
 // 32 rows at most: the four waves of a block share them and take every fourth
 // tile of 32 keys each, through LDS of their own, without a barrier until
-// their sums are joined at the end.
-template <int DP, bool MASKED>
+// their sums are joined at the end. REST: the rows of a few tiles that the
+// kernel above left, 32 to a block.
+template <int DP, bool MASKED, bool REST>
 __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) {
   constexpr int BQ = 32, UNIT = 128, kBytes = 32 * DP * 2, kUnits = DP / 8, kCopies = 32 * kUnits / 64;
   __shared__ __attribute__((aligned(16))) unsigned char ks[4 * kBytes], vs[4 * kBytes];
   __shared__ float ms[4][32], ls[4][32];
-  Division<BQ, UNIT> division(a);
   Work w;
-  const int block = blockIdx.x, whole = division.whole;
-  if (!division.find(block < whole ? block : -1, block - whole, w)) return;
-  w = uniform(w);
+  if constexpr (REST) {
+    Division<256, 64> division(a);
+    if (!division.find(a.rest_from + (int)blockIdx.x / 8, 0, w)) return;
+    w = uniform(w);
+    w.tile = w.tile * 8 + (int)blockIdx.x % 8;
+    if (w.tile * BQ >= w.s.rows) return;
+  } else {
+    Division<BQ, UNIT> division(a);
+    const int block = blockIdx.x, whole = division.whole;
+    if (!division.find(block < whole ? block : -1, block - whole, w)) return;
+    w = uniform(w);
+  }
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   State<DP, 1> st;
-  load_q<DP, 1>(a, w, w.tile * BQ, st);
-#pragma unroll
-  for (int j = 0; j < DP / 32; ++j) st.o[0][j] = f32x16{};
+  // units are of 64 keys in the kernel above
+  const int end = REST ? w.s.keys : min(w.unit1 * UNIT, w.s.keys);
   const float c = __uint_as_float(uniform((int)__float_as_uint(a.scale * 1.4426950408889634f)));
   unsigned char *const kb = ks + wave * kBytes, *const vb = vs + wave * kBytes;
   // copy i of the wave: unit 64 i + lane of its tile
@@ -816,37 +832,44 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
       dma16(r, in ? (int)(row * ld + u * 8) * 2 : kOut, 0, to + i * 1024);
     }
   };
-  const int end = min(w.unit1 * UNIT, w.s.keys);
-  int at = w.unit0 * UNIT + 32 * wave;
+  int at = REST ? 32 * wave : w.unit0 * UNIT + 32 * wave;
+  int byte = 0, byte_next = 0;
+  uint32_t keep = 0;
   if (at < end) {
-    int byte = 0, byte_next = 0;
     if constexpr (MASKED) {
       byte = mask_byte(a, w, at);
       byte_next = mask_byte(a, w, at + 128);
     }
-    uint32_t keep = (uint32_t)kept<MASKED>(a, w, at, byte);
+    keep = (uint32_t)kept<MASKED>(a, w, at, byte);
     copy(a.k, a.k_ld, true, kb, at, keep);
+  }
+  load_q<DP, 1>(a, w, w.tile * BQ, st);
+#pragma unroll
+  for (int j = 0; j < DP / 32; ++j) st.o[0][j] = f32x16{};
+  if (at < end) {
     copy(a.v, a.v_ld, false, vb, at, keep);
     for (; at < end; at += 128) {
-      const bool more = at + 128 < end;
-      uint32_t keep_next = 0;
-      if (more) {
-        keep_next = (uint32_t)kept<MASKED>(a, w, at + 128, byte_next);
-        if constexpr (MASKED) byte_next = mask_byte(a, w, at + 256);
-      }
+      // K of the next tile is requested behind this one's scores and V behind its outputs, always, so that what
+      // has landed can be counted
+      const uint32_t keep_next = (uint32_t)kept<MASKED>(a, w, at + 128, byte_next);
       f32x16 s[1];
       bf16x8 p[1][2];
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_waitcnt((kCopies & 0xF) | ((kCopies >> 4) << 14) | 0xF70);  // all but V
+      asm volatile("" ::: "memory");
       scores<DP, 1>(kb, 0, st, s);
       // the reads of K are back before its place is filled again
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (more) copy(a.k, a.k_ld, true, kb, at + 128, keep_next);
+      if constexpr (MASKED) byte_next = mask_byte(a, w, at + 256);
+      copy(a.k, a.k_ld, true, kb, at + 128, keep_next);
       weights<DP, 1>(st, s, c, keep, p);
+      __builtin_amdgcn_s_waitcnt((kCopies & 0xF) | ((kCopies >> 4) << 14) | 0xF70);  // all but the next K
+      asm volatile("" ::: "memory");
       outputs<DP, 1>(vb, 0, st, p);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (more) copy(a.v, a.v_ld, false, vb, at + 128, keep_next);
+      copy(a.v, a.v_ld, false, vb, at + 128, keep_next);
       keep = keep_next;
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // what was requested past the end
   }
   // Joined through the waves' own LDS: the first half of the outputs in K's place, the second in V's.
   const int h = lane >> 5, col = lane & 31;
@@ -864,76 +887,78 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
     ls[wave][col] = l;
   }
   __syncthreads();
-  const int rt = threadIdx.x & 31, r = w.tile * BQ + rt;
-  if (r >= w.s.rows) return;
-  float f[4], m = kLowest, sum = 0.f;
+  const int rows = min(w.s.rows - w.tile * BQ, BQ);
+  float *const part = w.slot >= 0 ? slot_at<DP, BQ>(a, w.slot) : nullptr;
+  for (int n = threadIdx.x; n < rows * (DP / 4); n += 256) {
+    const int d4 = (unsigned)n / (unsigned)rows, rt = n - d4 * rows;
+    float f[4], m = kLowest, sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = fmaxf(m, ms[i][rt]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = __builtin_amdgcn_exp2f(ms[i][rt] - m);
-    sum += ls[i][rt] * f[i];
-  }
-  float *part = w.slot >= 0 ? slot_at<DP, BQ>(a, w.slot) : nullptr;
-  if (part && threadIdx.x < 32) {
-    part[BQ * DP + rt] = m;
-    part[BQ * (DP + 1) + rt] = sum;
-  }
-  const float inv = reciprocal(sum);
-  uint16_t *o = out_row(a, w, r);
-  for (int d4 = threadIdx.x >> 5; d4 < DP / 4; d4 += 8) {
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, ms[i][rt]);
     const f32x4 *from = reinterpret_cast<const f32x4 *>(d4 < DP / 8 ? ks : vs) + (d4 % (DP / 8)) * 32 + rt;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      f[i] = __builtin_amdgcn_exp2f(ms[i][rt] - m);
+      sum = __builtin_fmaf(ls[i][rt], f[i], sum);
       const f32x4 x = from[i * (kBytes / 16)];
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(x[e], f[i], v[e]);
     }
-    if (part) *reinterpret_cast<f32x4 *>(part + ((int64_t)d4 * BQ + rt) * 4) = v;
-    else if (d4 * 4 < a.D)
-      *reinterpret_cast<u32x2 *>(o + d4 * 4) = u32x2{pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv)};
+    if (part) {
+      *reinterpret_cast<f32x4 *>(part + (d4 * BQ + rt) * 4) = v;
+      if (d4 == 0) {
+        part[BQ * DP + rt] = m;
+        part[BQ * (DP + 1) + rt] = sum;
+      }
+    } else if (d4 * 4 < a.D) {
+      const float inv = reciprocal(sum);
+      *reinterpret_cast<u32x2 *>(out_row(a, w, w.tile * BQ + rt) + d4 * 4) =
+          u32x2{pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv)};
+    }
   }
 }
 
 // ------------------------------------------------------------------ joining pieces
 
-// The pieces of the cut tiles become outputs. Grid: x cut tiles, y ranges of
-// 16 values; a thread has one row.
+// The pieces of the cut tiles become outputs. Grid: x cut tiles, y parts of
+// their work; a thread has one row at a time and 16 of its values.
 template <int DP, int BQ, int UNIT>
-__global__ __launch_bounds__(BQ < 64 ? 64 : BQ) void attention_join_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
   Division<BQ, UNIT> division(a);
   Work w;
   if (!division.find(division.whole + (int)blockIdx.x, 0, w) || w.slot < 0) return;
   w = uniform(w);
-  const int rt = threadIdx.x % BQ, r = w.tile * BQ + rt;
-  if (r >= w.s.rows) return;
-  const int pieces = w.parts;
-  const float *part = slot_at<DP, BQ>(a, w.slot);
-  constexpr int64_t kSlot = BQ * (DP + 2);
-  float m = kLowest, sum = 0.f;
-  for (int i = 0; i < pieces; ++i) m = fmaxf(m, part[i * kSlot + BQ * DP + rt]);
-  // 32 rows: two threads of a row share its values
-  constexpr int kShare = BQ < 64 ? 64 / BQ : 1;
-  const int d0 = blockIdx.y * 4 + threadIdx.x / BQ;
-  f32x4 v[4 / kShare] = {};
-  for (int i = 0; i < pieces; ++i) {
-    const float f = __builtin_amdgcn_exp2f(part[i * kSlot + BQ * DP + rt] - m);
-    sum = __builtin_fmaf(part[i * kSlot + BQ * (DP + 1) + rt], f, sum);
+  const int rows = min(w.s.rows - w.tile * BQ, BQ), pieces = w.parts;
+  const float *const part = slot_at<DP, BQ>(a, w.slot);
+  constexpr int kSlot = BQ * (DP + 2);
+  for (int n = blockIdx.y * 256 + threadIdx.x; n < rows * (DP / 16); n += 256 * gridDim.y) {
+    const int d16 = (unsigned)n / (unsigned)rows, rt = n - d16 * rows;
+    if (d16 * 16 >= a.D) break;
+    const float *from = part + (d16 * 4 * BQ + rt) * 4, *stats = part + BQ * DP + rt;
+    float m = kLowest, sum = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) m = fmaxf(m, stats[(int64_t)i * kSlot]);
+    f32x4 v[4] = {};
+#pragma unroll 2
+    for (int i = 0; i < pieces; ++i) {
+      const int64_t at = (int64_t)i * kSlot;
+      const float f = __builtin_amdgcn_exp2f(stats[at] - m);
+      sum = __builtin_fmaf(stats[at + BQ], f, sum);
 #pragma unroll
-    for (int j = 0; j < 4 / kShare; ++j) {
-      const f32x4 x = *reinterpret_cast<const f32x4 *>(part + i * kSlot + ((int64_t)(d0 + j * kShare) * BQ + rt) * 4);
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(from + at + j * BQ * 4);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[j][e] = __builtin_fmaf(x[e], f, v[j][e]);
+        for (int e = 0; e < 4; ++e) v[j][e] = __builtin_fmaf(x[e], f, v[j][e]);
+      }
     }
-  }
-  const float inv = reciprocal(sum);
-  uint16_t *o = out_row(a, w, r);
+    const float inv = reciprocal(sum);
+    uint16_t *o = out_row(a, w, w.tile * BQ + rt) + d16 * 16;
 #pragma unroll
-  for (int j = 0; j < 4 / kShare; ++j) {
-    const int d = 4 * (d0 + j * kShare);
-    if (d < a.D)
-      *reinterpret_cast<u32x2 *>(o + d) = u32x2{pack_bf16(v[j][0] * inv, v[j][1] * inv), pack_bf16(v[j][2] * inv, v[j][3] * inv)};
+    for (int j = 0; j < 4; j += 2)
+      if (d16 * 16 + j * 4 < a.D)
+        *reinterpret_cast<u32x4 *>(o + j * 4) =
+            u32x4{pack_bf16(v[j][0] * inv, v[j][1] * inv), pack_bf16(v[j][2] * inv, v[j][3] * inv),
+                  pack_bf16(v[j + 1][0] * inv, v[j + 1][1] * inv), pack_bf16(v[j + 1][2] * inv, v[j + 1][3] * inv)};
   }
 }
 
@@ -941,45 +966,93 @@ int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 constexpr int kCus = 256;  // MI355X
 
+// Parts of a cut tile's join: at most 256 threads' work each.
+template <int DP, int BQ> constexpr int kJoinParts = BQ * (DP / 16) > 256 ? BQ * (DP / 16) / 256 : 1;
+
 template <int DP, int NQ>
 void launch_rows(const AttentionArgs &a, const AttentionPlan &p, hipStream_t stream) {
   const dim3 grid((unsigned)p.blocks);
   if (a.key_mask) attention_kernel<DP, NQ, true><<<grid, 256, 0, stream>>>(a);
   else attention_kernel<DP, NQ, false><<<grid, 256, 0, stream>>>(a);
-  if (a.slots) attention_join_kernel<DP, 128 * NQ, 64><<<dim3((unsigned)p.cut, DP / 16), 128 * NQ, 0, stream>>>(a);
+  if (p.cut) attention_join_kernel<DP, 128 * NQ, 64><<<dim3((unsigned)p.cut, kJoinParts<DP, 128 * NQ>), 256, 0, stream>>>(a);
+}
+
+template <int DP, bool REST>
+void launch_few(const AttentionArgs &a, int64_t blocks, hipStream_t stream) {
+  const dim3 grid((unsigned)blocks);
+  if (a.key_mask) attention_few_kernel<DP, true, REST><<<grid, 256, 0, stream>>>(a);
+  else attention_few_kernel<DP, false, REST><<<grid, 256, 0, stream>>>(a);
 }
 
 template <int DP>
 void launch_width(const AttentionArgs &a, const AttentionPlan &p, hipStream_t stream) {
   if (p.rows == 32) {
-    const dim3 grid((unsigned)p.blocks);
-    if (a.key_mask) attention_few_kernel<DP, true><<<grid, 256, 0, stream>>>(a);
-    else attention_few_kernel<DP, false><<<grid, 256, 0, stream>>>(a);
-    if (a.slots) attention_join_kernel<DP, 32, 128><<<dim3((unsigned)p.cut, DP / 16), 64, 0, stream>>>(a);
+    launch_few<DP, false>(a, p.blocks, stream);
+    if (p.cut) attention_join_kernel<DP, 32, 128><<<dim3((unsigned)p.cut, kJoinParts<DP, 32>), 256, 0, stream>>>(a);
   } else if (p.rows == 128) {
     launch_rows<DP, 1>(a, p, stream);
-  } else {
+  } else if constexpr (DP != 128) {
     launch_rows<DP, 2>(a, p, stream);
+    if constexpr (DP == 256) {
+      if (p.rest) launch_few<DP, true>(a, p.rest * 8, stream);
+    }
   }
 }
 
 }  // namespace
 
-AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, int q_heads, int kv_heads, int D, bool workspace) {
+AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, bool offsets, int q_heads, int kv_heads, int D,
+                             bool workspace) {
   AttentionPlan p{};
   const int dp = padded(D);
-  const int64_t rows = Mq * (q_heads / kv_heads), each = rows / std::max<int64_t>(samples, 1);
-  p.rows = each <= 32 ? 32 : each <= 128 ? 128 : 256;
-  // tiles of all samples at most: whatever the offsets are, one more per sample than without them
-  const int64_t tiles = ((rows + p.rows - 1) / p.rows + samples) * kv_heads;
-  p.slots = workspace ? (p.rows == 32 ? 2 * kCus : kCus) : 0;
+  const int64_t rows = Mq * (q_heads / kv_heads), several = std::max<int64_t>(samples, 1);
+  const int64_t each = rows / several, keys = Mk / several;
+  auto tiles_of = [&](int64_t tile) {
+    // of all samples at most: whatever the offsets are, one more per sample than without them
+    const int64_t run = (rows + tile - 1) / tile;
+    return (offsets ? run + samples : run) * kv_heads;
+  };
+  // Rows of a tile. Up to 32 the waves of a block share the keys instead of
+  // the rows. 64 rows per wave read LDS half as often as 32, but leave one
+  // block to a CU. Heads of 256: 2048 rows of 16 heads over 300 keys 33 us
+  // with 64 rows and 23 with 32, 4000 keys 152 and 143, 16000 keys 479 and
+  // 512; 8192 rows 441 and 509 (4000 keys). Heads of 64: 16896 tokens of 18
+  // heads 1420 and 1544, 3000 rows of 16 heads over 4000 keys 84 and 85, over
+  // 1000 keys 37 and 30, 256 rows over 4000 keys 29 and 22. Heads of 128: two blocks of 32 rows per wave on a CU
+  // are as fast as one of 64 on the largest (2581 and 2591) and faster on all
+  // others.
+  if (each <= 32) p.rows = 32;
+  else if (each <= 128 || dp == 128) p.rows = 128;
+  else if (dp == 64) p.rows = 2 * tiles_of(256) >= kCus && keys >= 4000 ? 256 : 128;
+  else p.rows = 2 * tiles_of(256) > kCus || keys >= 8000 ? 256 : 128;
+  // blocks that a CU holds at once, by LDS and registers
+  const int held = p.rows == 32 ? (dp == 64 ? 4 : dp == 128 ? 2 : 1) : dp == 256 ? 1 : 2;
+  const int at_once = kCus * held;
+  const int64_t tiles = tiles_of(p.rows);
+  // Cutting pays for its second launch from some keys on (units of 128 with
+  // 32 rows, else of 64). One query of 16 heads of 256, whole and cut: 512
+  // keys 11 and 13 us, 1024 keys 17 and 15, 4096 keys 50 and 21; of 64: 1024
+  // keys 7.9 and 9.2, 4096 keys 21 and 11. 256 rows of 16 heads of 256: 300
+  // keys 18 and 22, 1000 keys 41 and 25.
   p.cut_all = p.rows == 32;
-  p.least_units = 4;
-  // keys that do not reach two pieces are not cut, nor are tiles that fill the blocks several times over
-  if (Mk <= (p.rows == 32 ? 128 : 64) * (int64_t)p.least_units || (p.cut_all && tiles >= 4 * (int64_t)p.slots)) p.slots = 0;
-  p.cut = p.slots == 0 ? 0 : p.cut_all ? tiles : std::min<int64_t>(tiles, p.slots - 1);
-  p.pieces = p.slots == 0 ? 0 : p.slots + p.cut;
-  p.blocks = tiles + p.pieces;
+  p.least_units = p.cut_all ? 2 : 3;
+  p.cut_units = !p.cut_all ? 10 : dp == 256 ? 8 : 16;
+  p.slots = workspace ? (p.cut_all ? std::max(at_once, 2 * kCus) : at_once) : 0;
+  // nor are tiles cut that fill the blocks several times over
+  if (Mk <= (p.cut_all ? 128 : 64) * (int64_t)(p.cut_units - 1) || (p.cut_all && tiles >= 4 * (int64_t)p.slots)) p.slots = 0;
+  // The last tiles of one sample over few keys: 32 rows to a block (8 of a
+  // tile) need no second launch to join them and fill the card where cutting
+  // the keys does not: 4096 rows of 18 heads of 256 over 512 keys (32 tiles
+  // behind 256 whole ones) 66 us, keys cut 82.
+  const int64_t behind = tiles % at_once;
+  if (!offsets && dp == 256 && p.rows == 256 && tiles > at_once && behind > 0 && behind * 8 <= at_once && Mk <= 2048) {
+    p.rest = behind;
+    p.rest_from = (int)(tiles - behind);
+    p.slots = 0;
+  }
+  if (p.slots > 0) p.cut = p.cut_all ? tiles : offsets ? std::min<int64_t>(tiles, p.slots - 1) : tiles % p.slots;
+  p.pieces = p.cut == 0 ? 0 : p.slots + p.cut;
+  p.blocks = tiles - p.rest + p.pieces;
   p.partial_bytes = (size_t)p.pieces * p.rows * (dp + 2) * sizeof(float);
   return p;
 }
@@ -989,7 +1062,9 @@ hipError_t launch_attention(const AttentionArgs &args, const AttentionPlan &p, h
   a.slots = p.slots;
   a.cut_all = p.cut_all;
   a.least_units = p.least_units;
+  a.cut_units = p.cut_units;
   a.pieces = p.pieces;
+  a.rest_from = p.rest_from;
   switch (padded(a.D)) {
     case 64: launch_width<64>(a, p, stream); break;
     case 128: launch_width<128>(a, p, stream); break;

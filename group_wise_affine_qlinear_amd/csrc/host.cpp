@@ -1146,7 +1146,7 @@ int attention_sizes(int64_t Mq, int64_t Mk, int64_t samples, int64_t q_heads, in
   if (!head_dim_ok(D) || samples > kMaxSamples || Mk > kMaxAttentionRows ||
       Mq > kMaxAttentionRows / (q_heads / kv_heads))
     return QL_EUNSUPPORTED;
-  const ql::AttentionPlan p = ql::attention_plan(Mq, Mk, samples, (int)q_heads, (int)kv_heads, (int)D, true);
+  const ql::AttentionPlan p = ql::attention_plan(Mq, Mk, samples, true, (int)q_heads, (int)kv_heads, (int)D, true);
   return p.blocks > kMaxBlocks ? QL_EUNSUPPORTED : QL_OK;
 }
 
@@ -1155,7 +1155,13 @@ int attention_sizes(int64_t Mq, int64_t Mk, int64_t samples, int64_t q_heads, in
 QL_API size_t qlinear_attention_workspace_bytes(int64_t Mq, int64_t Mk, int64_t samples, int64_t q_heads,
                                                 int64_t kv_heads, int64_t head_dim) {
   if (attention_sizes(Mq, Mk, samples, q_heads, kv_heads, head_dim) != QL_OK || Mq == 0 || samples == 0) return 0;
-  return ql::attention_plan(Mq, Mk, samples, (int)q_heads, (int)kv_heads, (int)head_dim, true).partial_bytes;
+  // with one sample there may be offsets or none
+  size_t bytes = 0;
+  for (const bool offsets : {false, true}) {
+    if (!offsets && samples > 1) continue;
+    bytes = std::max(bytes, ql::attention_plan(Mq, Mk, samples, offsets, (int)q_heads, (int)kv_heads, (int)head_dim, true).partial_bytes);
+  }
+  return bytes;
 }
 
 QL_API int qlinear_attention(const ql_attention_args *a, void *stream) {
@@ -1176,8 +1182,8 @@ QL_API int qlinear_attention(const ql_attention_args *a, void *stream) {
   if (a->q_ld > kMaxAttentionPitch || a->out_ld > kMaxAttentionPitch ||
       (a->Mk > 0 && (a->k_ld > kMaxAttentionPitch || a->v_ld > kMaxAttentionPitch)))
     return QL_EUNSUPPORTED;
-  const ql::AttentionPlan p = ql::attention_plan(a->Mq, a->Mk, samples, (int)a->q_heads, (int)a->kv_heads,
-                                                 (int)a->head_dim, a->workspace != nullptr);
+  const ql::AttentionPlan p = ql::attention_plan(a->Mq, a->Mk, samples, a->q_offsets != nullptr, (int)a->q_heads,
+                                                 (int)a->kv_heads, (int)a->head_dim, a->workspace != nullptr);
   if (a->workspace && a->workspace_bytes < p.partial_bytes) return QL_EWORKSPACE;
   ql::AttentionArgs k{};
   k.q = static_cast<const uint16_t *>(a->q);
@@ -1200,7 +1206,7 @@ QL_API int qlinear_attention(const ql_attention_args *a, void *stream) {
   k.key_mask = a->Mk > 0 ? a->key_mask : nullptr;
   k.partial = static_cast<float *>(a->workspace);
   char buf[160];
-  std::snprintf(buf, sizeof(buf), "attention_rows%d_slots%d", p.rows, p.slots);
+  std::snprintf(buf, sizeof(buf), "attention_rows%d_slots%d%s", p.rows, p.slots, p.rest ? "_rest32" : "");
   set_last_path(buf);
   return ql::launch_attention(k, p, reinterpret_cast<hipStream_t>(stream)) == hipSuccess ? QL_OK : QL_EHIP;
 }

@@ -233,7 +233,8 @@ struct AttentionArgs {
   const uint8_t *key_mask;               // or null
   float *partial;                        // workspace
   // set by launch_attention from the plan
-  int slots, cut_all, least_units;
+  int slots, cut_all, least_units, cut_units;
+  int rest_from;
   int64_t pieces;
 };
 // How a call's tiles are divided over blocks, as far as the sizes alone say it.
@@ -241,12 +242,16 @@ struct AttentionPlan {
   int rows;              // query rows of a tile: 32, 128 or 256
   int slots;             // blocks that the keys of cut tiles are divided over; 0: none is cut
   int cut_all;           // 1: all tiles, 0: those behind the last multiple of slots
-  int least_units;       // units of keys of a piece at least
+  int least_units;       // units of keys of a piece at least, where a sample has enough
+  int cut_units;         // units of keys from which a tile is cut
   int64_t cut, pieces;   // cut tiles and their pieces at most
+  int64_t rest;          // last tiles that go 32 rows to a block instead, from tile rest_from on
+  int rest_from;
   int64_t blocks;        // tiles and pieces at most
   size_t partial_bytes;
 };
-AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, int q_heads, int kv_heads, int D, bool workspace);
+AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, bool offsets, int q_heads, int kv_heads, int D,
+                             bool workspace);
 hipError_t launch_attention(const AttentionArgs &a, const AttentionPlan &p, hipStream_t stream);
 
 }  // namespace ql

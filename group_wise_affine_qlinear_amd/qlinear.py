@@ -803,14 +803,22 @@ def qlinear_adapters(x, a, b, row_adapter, M, N, K, out, *, y=None, ranks=None, 
 
 # ------------------------------------------------------------------ between QKV and output projection
 
-def _heads(torch, t, name, dtypes, rows, D, device):
+def _heads(torch, t, name, dtype, rows, D, device):
     """(pointer, row pitch, heads) of a [rows, heads, D] tensor whose rows may be slices of longer ones."""
+    try:
+        # what nearly every call passes, in as few steps as tell it
+        n, heads, d = t.shape
+        pitch, head, step = t.stride()
+        if step == 1 and head == D == d and n == rows and pitch >= heads * D and t.dtype is dtype and t.device == device:
+            return t.data_ptr(), pitch if n > 1 else heads * D, heads
+    except (AttributeError, TypeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     shape = t.shape
     if len(shape) != 3 or shape[0] != rows or shape[2] != D:
         raise ValueError(f"{name} has shape {tuple(shape)}, expected [{rows}, heads, {D}]")
@@ -819,7 +827,7 @@ def _heads(torch, t, name, dtypes, rows, D, device):
     width = heads * D
     if rows > 0 and ((D > 1 and step != 1) or (heads > 1 and head != D) or (rows > 1 and pitch < width)):
         raise ValueError(f"{name} must have rows of consecutive heads that do not overlap")
-    return t.data_ptr(), pitch if rows > 1 else width, heads
+    return t.data_ptr(), pitch if rows > 1 and pitch > width else width, heads
 
 
 def qlinear_qk_norm_rope(M, head_dim, *, q=None, k=None, v=None, q_out=None, k_out=None, v_out=None,
@@ -846,31 +854,35 @@ def qlinear_qk_norm_rope(M, head_dim, *, q=None, k=None, v=None, q_out=None, k_o
     a = ql_qk_args()
     a.M, a.head_dim, a.norm, a.eps, a.rope = M, head_dim, norm, eps, rope
     a.in_dtype = _value_dtype(torch, first, "q, k and v")
-    one, bf16, f32, i32 = (first.dtype,), (torch.bfloat16,), (torch.float32,), (torch.int32,)
+    one, bf16, f32, i32 = first.dtype, torch.bfloat16, (torch.float32,), (torch.int32,)
     if q is not None:
-        a.q, a.q_ld, a.q_heads = _heads(torch, q, "q", one, M, head_dim, dev)
-        a.q_out, a.q_out_ld, heads = _heads(torch, q_out, "q_out", bf16, M, head_dim, dev)
-        if heads != a.q_heads:
+        a.q, a.q_ld, heads = _heads(torch, q, "q", one, M, head_dim, dev)
+        a.q_out, a.q_out_ld, out_heads = _heads(torch, q_out, "q_out", bf16, M, head_dim, dev)
+        if out_heads != heads:
             raise ValueError("q_out must have the shape of q")
+        a.q_heads = heads
     elif q_out is not None:
         raise ValueError("q_out without q")
+    kv_heads = None
     if k is not None:
-        a.k, a.k_ld, a.kv_heads = _heads(torch, k, "k", one, M, head_dim, dev)
-        a.k_out, a.k_out_ld, heads = _heads(torch, k_out, "k_out", bf16, M, head_dim, dev)
-        if heads != a.kv_heads:
+        a.k, a.k_ld, kv_heads = _heads(torch, k, "k", one, M, head_dim, dev)
+        a.k_out, a.k_out_ld, out_heads = _heads(torch, k_out, "k_out", bf16, M, head_dim, dev)
+        if out_heads != kv_heads:
             raise ValueError("k_out must have the shape of k")
     elif k_out is not None:
         raise ValueError("k_out without k")
     if v is not None:
         a.v, a.v_ld, heads = _heads(torch, v, "v", one, M, head_dim, dev)
-        if k is not None and heads != a.kv_heads:
+        a.v_out, a.v_out_ld, out_heads = _heads(torch, v_out, "v_out", bf16, M, head_dim, dev)
+        if k is not None and heads != kv_heads:
             raise ValueError("k and v must have the same heads")
-        a.kv_heads = heads
-        a.v_out, a.v_out_ld, heads = _heads(torch, v_out, "v_out", bf16, M, head_dim, dev)
-        if heads != a.kv_heads:
+        if out_heads != heads:
             raise ValueError("v_out must have the shape of v")
+        kv_heads = heads
     elif v_out is not None:
         raise ValueError("v_out without v")
+    if kv_heads is not None:
+        a.kv_heads = kv_heads
     if q_weight is not None:
         a.q_weight = _operand(q_weight, "q_weight", f32, (head_dim,), dev)
     if k_weight is not None:
@@ -922,17 +934,19 @@ def qlinear_attention(q, k, v, out, *, scale=None, q_offsets=None, k_offsets=Non
     if dev.type != "cuda":
         raise ValueError("q must be a device tensor")
     a = ql_attention_args()
-    bf16, i32 = (torch.bfloat16,), (torch.int32,)
-    a.Mq, a.Mk, a.head_dim = q.shape[0], k.shape[0], q.shape[2]
-    a.q, a.q_ld, a.q_heads = _heads(torch, q, "q", bf16, a.Mq, a.head_dim, dev)
-    a.k, a.k_ld, a.kv_heads = _heads(torch, k, "k", bf16, a.Mk, a.head_dim, dev)
-    a.v, a.v_ld, heads = _heads(torch, v, "v", bf16, a.Mk, a.head_dim, dev)
-    if heads != a.kv_heads:
+    bf16, i32 = torch.bfloat16, (torch.int32,)
+    Mq, q_heads, D = q.shape
+    Mk, kv_heads, _ = k.shape
+    a.Mq, a.Mk, a.q_heads, a.kv_heads, a.head_dim = Mq, Mk, q_heads, kv_heads, D
+    a.q, a.q_ld, _ = _heads(torch, q, "q", bf16, Mq, D, dev)
+    a.k, a.k_ld, _ = _heads(torch, k, "k", bf16, Mk, D, dev)
+    a.v, a.v_ld, heads = _heads(torch, v, "v", bf16, Mk, D, dev)
+    if heads != kv_heads:
         raise ValueError("k and v must have the same heads")
-    a.out, a.out_ld, heads = _heads(torch, out, "out", bf16, a.Mq, a.head_dim, dev)
-    if heads != a.q_heads:
+    a.out, a.out_ld, heads = _heads(torch, out, "out", bf16, Mq, D, dev)
+    if heads != q_heads:
         raise ValueError("out must have the shape of q")
-    a.scale = max(a.head_dim, 1) ** -0.5 if scale is None else scale
+    a.scale = max(D, 1) ** -0.5 if scale is None else scale
     samples = 1
     if (q_offsets is None) != (k_offsets is None):
         raise ValueError("q_offsets and k_offsets must be given together")
@@ -945,11 +959,11 @@ def qlinear_attention(q, k, v, out, *, scale=None, q_offsets=None, k_offsets=Non
         a.q_offsets = _operand(q_offsets, "q_offsets", i32, q_offsets.shape, dev)
         a.k_offsets = _operand(k_offsets, "k_offsets", i32, q_offsets.shape, dev)
     if key_mask is not None:
-        a.key_mask = _operand(key_mask, "key_mask", (torch.bool, torch.uint8), (a.Mk,), dev)
+        a.key_mask = _operand(key_mask, "key_mask", (torch.bool, torch.uint8), (Mk,), dev)
     if isinstance(workspace, str):
         if workspace != TORCH_WORKSPACE:
             raise ValueError(f"workspace must be a device tensor, None or {TORCH_WORKSPACE!r}")
-        nbytes = lib.qlinear_attention_workspace_bytes(a.Mq, a.Mk, samples, a.q_heads, a.kv_heads, a.head_dim)
+        nbytes = lib.qlinear_attention_workspace_bytes(Mq, Mk, samples, q_heads, kv_heads, D)
         workspace = _empty(torch, nbytes, torch.uint8, dev, stream) if nbytes else None
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor):

@@ -112,6 +112,8 @@ SIZES = [
     # queries, keys, query heads, key heads, D: tiles of each height with ends inside, one key, one query, odd groups
     (1, 1, 1, 1, 8), (1, 33, 2, 1, 64), (5, 31, 2, 2, 72), (32, 64, 1, 1, 128), (33, 65, 2, 1, 40), (130, 257, 3, 1, 64),
     (128, 128, 2, 2, 256), (7, 700, 6, 2, 136), (300, 1, 2, 2, 128), (257, 321, 2, 2, 128), (513, 200, 1, 1, 256),
+    # tiles behind as many as the card holds, which go 32 rows to a block
+    (2500, 70, 26, 26, 128), (1290, 40, 43, 43, 256),
     (260, 515, 2, 1, 96), (1, 5000, 4, 4, 256), (3, 9001, 8, 1, 64), (140, 3001, 2, 1, 256), (300, 2049, 1, 1, 64),
 ]
 
@@ -153,9 +155,9 @@ def test_ragged(torch, q_len, k_len, hq, hkv, D, masked):
     check(torch, q, k, v, q_len, k_len, mask, first=(4, 5))
 
 
-@pytest.mark.parametrize("nq,nk,D", [(3, 700, 64), (200, 300, 128), (300, 300, 256)])
-def test_masks(torch, nq, nk, D):
-    q, k, v = make(torch, nq, nk, 2, 1, D, 5)
+@pytest.mark.parametrize("nq,nk,D,heads", [(3, 700, 64, 2), (200, 300, 128, 2), (300, 300, 256, 2), (1290, 50, 256, 43)])
+def test_masks(torch, nq, nk, D, heads):
+    q, k, v = make(torch, nq, nk, heads, 1 if heads == 2 else heads, D, 5)
     for mask in (np.zeros(nk, bool), np.arange(nk) % 2 == 0, np.arange(nk) == nk - 1, np.arange(nk) >= 256,
                  np.ones(nk, bool), (np.arange(nk) % 3 * 100).astype(np.uint8)):
         check(torch, q, k, v, mask=mask)
