@@ -1038,8 +1038,11 @@ AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, bool offse
   p.least_units = p.cut_all ? 2 : 3;
   p.cut_units = !p.cut_all ? 10 : dp == 256 ? 8 : 16;
   p.slots = workspace ? (p.cut_all ? std::max(at_once, 2 * kCus) : at_once) : 0;
-  // nor are tiles cut that fill the blocks several times over
-  if (Mk <= (p.cut_all ? 128 : 64) * (int64_t)(p.cut_units - 1) || (p.cut_all && tiles >= 4 * (int64_t)p.slots)) p.slots = 0;
+  // Nor are tiles cut that fill the blocks several times over, or where a
+  // sample's keys are far below that on average (a batch of which one sample
+  // has most of the keys loses by that).
+  const int64_t cut_keys = (p.cut_all ? 128 : 64) * (int64_t)p.cut_units;
+  if (Mk < cut_keys || keys * 2 < cut_keys || (p.cut_all && tiles >= 4 * (int64_t)p.slots)) p.slots = 0;
   // The last tiles of one sample over few keys: 32 rows to a block (8 of a
   // tile) need no second launch to join them and fill the card where cutting
   // the keys does not: 4096 rows of 18 heads of 256 over 512 keys (32 tiles
