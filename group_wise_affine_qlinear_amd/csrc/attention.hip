@@ -41,6 +41,10 @@ constexpr int kOut = 0x7FFFFFFF;  // an offset past every buffer: the load gives
 __device__ __forceinline__ int k_unit(int row, int c) { return c ^ (row & 7); }
 __device__ __forceinline__ int v_unit(int row, int c) { return c ^ ((row & 3) * 2); }
 
+// Values of a row in LDS, whole groups of eight units, for heads of DP values
+// (D rounded up to what the kernels are made for).
+constexpr int lds_width(int DP) { return (DP + 63) / 64 * 64; }
+
 __device__ __forceinline__ bf16x8 lds_read8(const unsigned char *p) { return *reinterpret_cast<const bf16x8 *>(p); }
 
 __device__ __forceinline__ s16x4 lds_read_tr(const unsigned char *p) {
@@ -298,18 +302,18 @@ __device__ __forceinline__ void load_q(const AttentionArgs &a, const Work &w, in
   }
 }
 
-// S^T of 32 keys: K rows [row0, row0 + 32) of the stage at kb.
+// S^T of the 32 keys whose K rows are at kb.
 template <int DP, int NQ>
-__device__ __forceinline__ void scores(const unsigned char *kb, int row0, const State<DP, NQ> &st, f32x16 (&s)[NQ]) {
+__device__ __forceinline__ void scores(const unsigned char *kb, const State<DP, NQ> &st, f32x16 (&s)[NQ]) {
   const int lane = threadIdx.x & 63, row = lane & 31, h = lane >> 5;
 #pragma unroll
   for (int i = 0; i < NQ; ++i) s[i] = f32x16{};
   int base[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) base[j] = row * (DP * 2) + k_unit(row, 2 * j + h) * 16;
+  for (int j = 0; j < 4; ++j) base[j] = row * (lds_width(DP) * 2) + k_unit(row, 2 * j + h) * 16;
 #pragma unroll
   for (int j = 0; j < DP / 16; ++j) {
-    const bf16x8 k = lds_read8(kb + base[j & 3] + (row0 * DP * 2 + (j >> 2) * 128));
+    const bf16x8 k = lds_read8(kb + base[j & 3] + (j >> 2) * 128);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) s[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, st.q[i][j], s[i], 0, 0, 0);
   }
@@ -370,21 +374,21 @@ __device__ __forceinline__ void weights(State<DP, NQ> &st, f32x16 (&s)[NQ], floa
   }
 }
 
-// O^T += V^T P^T over the 32 V rows [row0, row0 + 32) of the stage at vb.
+// O^T += V^T P^T over the 32 V rows at vb.
 template <int DP, int NQ>
-__device__ __forceinline__ void outputs(const unsigned char *vb, int row0, State<DP, NQ> &st, const bf16x8 (&p)[NQ][2]) {
+__device__ __forceinline__ void outputs(const unsigned char *vb, State<DP, NQ> &st, const bf16x8 (&p)[NQ][2]) {
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int row = 4 * h + ((lane & 15) >> 2);                         // + 16 t + 8 u
   const int unit = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), byte = (lane & 1) * 8;  // + 4 j
   int base[2];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) base[j] = row * (DP * 2) + v_unit(row, unit + 4 * j) * 16 + byte;
+  for (int j = 0; j < 2; ++j) base[j] = row * (lds_width(DP) * 2) + v_unit(row, unit + 4 * j) * 16 + byte;
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int j = 0; j < DP / 32; ++j) {
-      const unsigned char *r = vb + base[j & 1] + ((row0 + 16 * t) * DP * 2 + (j >> 1) * 128);
-      const s16x4 lo = lds_read_tr(r), hi = lds_read_tr(r + 8 * DP * 2);
+      const unsigned char *r = vb + base[j & 1] + (16 * t * lds_width(DP) * 2 + (j >> 1) * 128);
+      const s16x4 lo = lds_read_tr(r), hi = lds_read_tr(r + 8 * lds_width(DP) * 2);
       const bf16x8 v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
       for (int i = 0; i < NQ; ++i) st.o[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[i][t], st.o[i][j], 0, 0, 0);
@@ -433,15 +437,16 @@ __device__ __forceinline__ float reciprocal(float l) { return l == 0.f ? 0.f : 1
 // offsets serve all of them.
 template <int DP>
 struct Lanes {
+  static constexpr int kRow = lds_width(DP) * 2;
   int k[4], v[2];
 
   __device__ __forceinline__ Lanes() {
     const int lane = threadIdx.x & 63, h = lane >> 5, row = lane & 31;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) k[j] = row * (DP * 2) + k_unit(row, 2 * j + h) * 16;
+    for (int j = 0; j < 4; ++j) k[j] = row * kRow + k_unit(row, 2 * j + h) * 16;
     const int vrow = 4 * h + ((lane & 15) >> 2), unit = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) v[j] = vrow * (DP * 2) + v_unit(vrow, unit + 4 * j) * 16 + (lane & 1) * 8;
+    for (int j = 0; j < 2; ++j) v[j] = vrow * kRow + v_unit(vrow, unit + 4 * j) * 16 + (lane & 1) * 8;
   }
   // 16 values of K's row at 16 j, of the 32 rows at kb
   __device__ __forceinline__ bf16x8 k_frag(const unsigned char *kb, int j) const {
@@ -450,8 +455,8 @@ struct Lanes {
   // V^T's rows 32 (f % (DP / 32)), of 16 of the 32 keys at vb
   __device__ __forceinline__ bf16x8 v_frag(const unsigned char *vb, int f) const {
     const int t = f / (DP / 32), j = f % (DP / 32);
-    const unsigned char *p = vb + v[j & 1] + (16 * t * DP * 2 + (j >> 1) * 128);
-    const s16x4 lo = lds_read_tr(p), hi = lds_read_tr(p + 8 * DP * 2);
+    const unsigned char *p = vb + v[j & 1] + (16 * t * kRow + (j >> 1) * 128);
+    const s16x4 lo = lds_read_tr(p), hi = lds_read_tr(p + 8 * kRow);
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 };
@@ -536,8 +541,8 @@ __device__ __forceinline__ void constants(F f) { constants(std::make_integer_seq
 // weights between the MFMAs; while these meet V, the next maximum is taken.
 template <int DP, int NQ, bool MASKED>
 __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
-  constexpr int BQ = 128 * NQ, UNIT = 64, kBytes = UNIT * DP * 2, kHalf = kBytes / 2;
-  constexpr int kUnits = DP / 8;                // 16-byte units of a row
+  constexpr int kRow = lds_width(DP) * 2, BQ = 128 * NQ, UNIT = 64, kBytes = UNIT * kRow, kHalf = kBytes / 2;
+  constexpr int kUnits = kRow / 16;             // 16-byte units of a row
   constexpr int kCopies = UNIT * kUnits / 256;  // copies of 64 units per wave and stage
   constexpr int kSteps = DP / 16, kFrags = DP / 16;
   __shared__ __attribute__((aligned(16))) unsigned char k0[kBytes], k1[kBytes], v0[kBytes], v1[kBytes];
@@ -554,32 +559,47 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
   const float c = __uint_as_float(uniform((int)__float_as_uint(a.scale * 1.4426950408889634f)));
   const Lanes<DP> at;
 
-  // copy i of this wave: unit (4 i + wave) * 64 + lane of the stage
-  constexpr int kRows = 256 / kUnits;  // rows from copy to copy, a multiple of 8: the units of a lane stay
-  const int row = (wave * 64 + lane) / kUnits;
-  const int kc = k_unit(row, lane % kUnits), vc = v_unit(row, lane % kUnits);
-  const int kofs = kc * 8 < a.D ? (int)(row * a.k_ld + kc * 8) * 2 : kOut;
-  const int vofs = vc * 8 < a.D ? (int)(row * a.v_ld + vc * 8) * 2 : kOut;
+  // Copy i of this wave: unit (4 i + wave) * 64 + lane of the stage. Every kKinds
+  // copies (one, or three of rows of 24 units) the units of a lane come again,
+  // kRows rows on, a multiple of 8.
+  constexpr int kKinds = kUnits == 24 ? 3 : 1, kRows = kKinds * 256 / kUnits;
+  int row[kKinds];
+  uint32_t kofs[kKinds], vofs[kKinds];
+#pragma unroll
+  for (int b = 0; b < kKinds; ++b) {
+    const int id = (4 * b + wave) * 64 + lane;
+    row[b] = id / kUnits;
+    const int kc = k_unit(row[b], id % kUnits), vc = v_unit(row[b], id % kUnits);
+    kofs[b] = kc * 8 < a.D ? (uint32_t)(row[b] * a.k_ld + kc * 8) * 2 : kOut;
+    vofs[b] = vc * 8 < a.D ? (uint32_t)(row[b] * a.v_ld + vc * 8) * 2 : kOut;
+  }
   const int first = w.unit0 * UNIT, end = min(w.unit1 * UNIT, w.s.keys);
   // The copies of one stage of K or V, requested one at a time.
   struct Copies {
     __amdgpu_buffer_rsrc_t rows;
-    uint32_t ofs, step;
+    uint32_t ofs[kKinds], step;
     unsigned char *to;
     uint64_t keep;
-    int row;
+    int row[kKinds];
     __device__ __forceinline__ void one(int i) {
-      dma16(rows, !MASKED || (keep >> (row + i * kRows) & 1) ? ofs : kOut, 0, to + i * 4096);
-      ofs += step;
+      const int b = i % kKinds;
+      dma16(rows, !MASKED || (keep >> (row[b] + i / kKinds * kRows) & 1) ? ofs[b] : kOut, 0, to + i * 4096);
+      ofs[b] += step;
     }
     __device__ __forceinline__ void all() {
 #pragma unroll
       for (int i = 0; i < kCopies; ++i) one(i);
     }
   };
-  auto copies = [&](const uint16_t *x, int64_t ld, int ofs, unsigned char *to, int from, uint64_t keep) __attribute__((always_inline)) {
-    Copies c = {rows_of(a, x, ld, w, from), (uint32_t)ofs, (uint32_t)(kRows * ld * 2), to + wave * 1024, keep, row};
-    asm volatile("" : "+v"(c.ofs));  // or every copy's offset is kept in a register over the loop
+  auto copies = [&](const uint16_t *x, int64_t ld, const uint32_t (&ofs)[kKinds], unsigned char *to, int from, uint64_t keep)
+      __attribute__((always_inline)) {
+    Copies c = {rows_of(a, x, ld, w, from), {}, (uint32_t)(kRows * ld * 2), to + wave * 1024, keep, {}};
+#pragma unroll
+    for (int b = 0; b < kKinds; ++b) {
+      c.ofs[b] = ofs[b];
+      c.row[b] = row[b];
+      asm volatile("" : "+v"(c.ofs[b]));  // or every copy's offset is kept in a register over the loop
+    }
     return c;
   };
   // Kept keys of the stages in hand; a stage's bytes of the mask are requested two stages ahead.
@@ -779,14 +799,14 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
     constants<4 * kTiles>([&](auto four) __attribute__((always_inline)) {
       constexpr int j = decltype(four)::value / 4, g = decltype(four)::value % 4;
       const f32x4 v = O::template get<i * kTiles + j, 4 * g>();
-      *reinterpret_cast<u32x2 *>(rows + q * (DP * 2) + (((4 * j + g) ^ q) & (kUnits - 1)) * 16 + h * 8) =
+      *reinterpret_cast<u32x2 *>(rows + q * kRow + ((4 * j + g) ^ (q & 7)) * 16 + h * 8) =
           u32x2{pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f)};
     });
   });
 #pragma unroll 4
   for (int n = 0; n < 32 * NQ * kUnits / 64; ++n) {
-    const int q = n * (64 / kUnits) + lane / kUnits, u = lane % kUnits;
-    const u32x4 v = *reinterpret_cast<const u32x4 *>(rows + q * (DP * 2) + ((u ^ q) & (kUnits - 1)) * 16);
+    const int q = (n * 64 + lane) / kUnits, u = (n * 64 + lane) % kUnits;
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(rows + q * kRow + (u ^ (q & 7)) * 16);
     if (r0 + q < w.s.rows && u * 8 < a.D) *reinterpret_cast<u32x4 *>(out_row(a, w, r0 + q) + u * 8) = v;
   }
 }
@@ -799,7 +819,8 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
 // kernel above left, 32 to a block.
 template <int DP, bool MASKED, bool REST>
 __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) {
-  constexpr int BQ = 32, UNIT = 128, kBytes = 32 * DP * 2, kUnits = DP / 8, kCopies = 32 * kUnits / 64;
+  constexpr int kRow = lds_width(DP) * 2, BQ = 32, UNIT = 128, kBytes = 32 * kRow, kUnits = kRow / 16;
+  constexpr int kCopies = 32 * kUnits / 64, kTiles = lds_width(DP) / 64;  // tiles of 32 values that K's place holds
   __shared__ __attribute__((aligned(16))) unsigned char ks[4 * kBytes], vs[4 * kBytes];
   __shared__ float ms[4][32], ls[4][32];
   Work w;
@@ -856,7 +877,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
       bf16x8 p[1][2];
       __builtin_amdgcn_s_waitcnt((kCopies & 0xF) | ((kCopies >> 4) << 14) | 0xF70);  // all but V
       asm volatile("" ::: "memory");
-      scores<DP, 1>(kb, 0, st, s);
+      scores<DP, 1>(kb, st, s);
       // the reads of K are back before its place is filled again
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if constexpr (MASKED) byte_next = mask_byte(a, w, at + 256);
@@ -864,7 +885,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
       weights<DP, 1>(st, s, c, keep, p);
       __builtin_amdgcn_s_waitcnt((kCopies & 0xF) | ((kCopies >> 4) << 14) | 0xF70);  // all but the next K
       asm volatile("" ::: "memory");
-      outputs<DP, 1>(vb, 0, st, p);
+      outputs<DP, 1>(vb, st, p);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       copy(a.v, a.v_ld, false, vb, at + 128, keep_next);
       keep = keep_next;
@@ -876,10 +897,10 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
   const float l = st.l[0] + other_half(st.l[0]);
 #pragma unroll
   for (int j = 0; j < DP / 32; ++j) {
-    f32x4 *const to = reinterpret_cast<f32x4 *>(j < DP / 64 ? kb : vb);
+    f32x4 *const to = reinterpret_cast<f32x4 *>(j < kTiles ? kb : vb);
 #pragma unroll
     for (int g = 0; g < 4; ++g)
-      to[(8 * (j % (DP / 64)) + 2 * g + h) * 32 + col] =
+      to[(8 * (j % kTiles) + 2 * g + h) * 32 + col] =
           f32x4{st.o[0][j][4 * g], st.o[0][j][4 * g + 1], st.o[0][j][4 * g + 2], st.o[0][j][4 * g + 3]};
   }
   if (h == 0) {
@@ -894,7 +915,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
     float f[4], m = kLowest, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) m = fmaxf(m, ms[i][rt]);
-    const f32x4 *from = reinterpret_cast<const f32x4 *>(d4 < DP / 8 ? ks : vs) + (d4 % (DP / 8)) * 32 + rt;
+    const f32x4 *from = reinterpret_cast<const f32x4 *>(d4 < 8 * kTiles ? ks : vs) + d4 % (8 * kTiles) * 32 + rt;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -962,7 +983,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
   }
 }
 
-int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+int padded(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : D <= 192 ? 192 : 256; }
 
 constexpr int kCus = 256;  // MI355X
 
@@ -991,7 +1012,7 @@ void launch_width(const AttentionArgs &a, const AttentionPlan &p, hipStream_t st
     if (p.cut) attention_join_kernel<DP, 32, 128><<<dim3((unsigned)p.cut, kJoinParts<DP, 32>), 256, 0, stream>>>(a);
   } else if (p.rows == 128) {
     launch_rows<DP, 1>(a, p, stream);
-  } else if constexpr (DP != 128) {
+  } else if constexpr (DP != 96 && DP != 128) {
     launch_rows<DP, 2>(a, p, stream);
     if constexpr (DP == 256) {
       if (p.rest) launch_few<DP, true>(a, p.rest * 8, stream);
@@ -1012,7 +1033,7 @@ AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, bool offse
     const int64_t run = (rows + tile - 1) / tile;
     return (offsets ? run + samples : run) * kv_heads;
   };
-  // Rows of a tile. Up to 32 the waves of a block share the keys instead of
+  // Rows of a tile (96 goes by 128, 192 by 256). Up to 32 the waves of a block share the keys instead of
   // the rows. 64 rows per wave read LDS half as often as 32, but leave one
   // block to a CU. Heads of 256: 2048 rows of 16 heads over 300 keys 33 us
   // with 64 rows and 23 with 32, 4000 keys 152 and 143, 16000 keys 479 and
@@ -1022,11 +1043,11 @@ AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, bool offse
   // are as fast as one of 64 on the largest (2581 and 2591) and faster on all
   // others.
   if (each <= 32) p.rows = 32;
-  else if (each <= 128 || dp == 128) p.rows = 128;
+  else if (each <= 128 || dp == 96 || dp == 128) p.rows = 128;
   else if (dp == 64) p.rows = 2 * tiles_of(256) >= kCus && keys >= 4000 ? 256 : 128;
   else p.rows = 2 * tiles_of(256) > kCus || keys >= 8000 ? 256 : 128;
   // blocks that a CU holds at once, by LDS and registers
-  const int held = p.rows == 32 ? (dp == 64 ? 4 : dp == 128 ? 2 : 1) : dp == 256 ? 1 : 2;
+  const int held = p.rows == 32 ? (dp == 64 ? 4 : dp <= 128 ? 2 : 1) : dp <= 128 ? 2 : 1;
   const int at_once = kCus * held;
   const int64_t tiles = tiles_of(p.rows);
   // Cutting pays for its second launch from some keys on (units of 128 with
@@ -1036,7 +1057,7 @@ AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, bool offse
   // keys 18 and 22, 1000 keys 41 and 25.
   p.cut_all = p.rows == 32;
   p.least_units = p.cut_all ? 2 : 3;
-  p.cut_units = !p.cut_all ? 10 : dp == 256 ? 8 : 16;
+  p.cut_units = !p.cut_all ? 10 : dp > 128 ? 8 : 16;
   p.slots = workspace ? (p.cut_all ? std::max(at_once, 2 * kCus) : at_once) : 0;
   // Nor are tiles cut that fill the blocks several times over, or where a
   // sample's keys are far below that on average (a batch of which one sample
@@ -1070,6 +1091,8 @@ hipError_t launch_attention(const AttentionArgs &args, const AttentionPlan &p, h
   a.rest_from = p.rest_from;
   switch (padded(a.D)) {
     case 64: launch_width<64>(a, p, stream); break;
+    case 96: launch_width<96>(a, p, stream); break;
+    case 192: launch_width<192>(a, p, stream); break;
     case 128: launch_width<128>(a, p, stream); break;
     default: launch_width<256>(a, p, stream); break;
   }

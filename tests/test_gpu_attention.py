@@ -114,7 +114,7 @@ SIZES = [
     (128, 128, 2, 2, 256), (7, 700, 6, 2, 136), (300, 1, 2, 2, 128), (257, 321, 2, 2, 128), (513, 200, 1, 1, 256),
     # tiles behind as many as the card holds, which go 32 rows to a block
     (2500, 70, 26, 26, 128), (1290, 40, 43, 43, 256),
-    (260, 515, 2, 1, 96), (1, 5000, 4, 4, 256), (3, 9001, 8, 1, 64), (140, 3001, 2, 1, 256), (300, 2049, 1, 1, 64),
+    (260, 515, 2, 1, 96), (400, 700, 2, 2, 192), (130, 300, 2, 1, 160), (9, 3000, 4, 2, 176), (700, 400, 20, 20, 184), (33, 1500, 2, 2, 88), (1, 5000, 4, 4, 256), (3, 9001, 8, 1, 64), (140, 3001, 2, 1, 256), (300, 2049, 1, 1, 64),
 ]
 
 
@@ -135,7 +135,7 @@ RAGGED = [
 
 
 @pytest.mark.parametrize("q_len,k_len", RAGGED)
-@pytest.mark.parametrize("hq,hkv,D", [(2, 2, 64), (4, 1, 128), (1, 1, 256), (6, 2, 72)])
+@pytest.mark.parametrize("hq,hkv,D", [(2, 2, 64), (4, 1, 128), (1, 1, 256), (6, 2, 72), (2, 2, 192)])
 @pytest.mark.parametrize("masked", [False, True])
 def test_ragged(torch, q_len, k_len, hq, hkv, D, masked):
     """Samples that begin behind rows of no sample and end before others, which stay as they were; what hidden keys,
@@ -155,7 +155,7 @@ def test_ragged(torch, q_len, k_len, hq, hkv, D, masked):
     check(torch, q, k, v, q_len, k_len, mask, first=(4, 5))
 
 
-@pytest.mark.parametrize("nq,nk,D,heads", [(3, 700, 64, 2), (200, 300, 128, 2), (300, 300, 256, 2), (1290, 50, 256, 43)])
+@pytest.mark.parametrize("nq,nk,D,heads", [(3, 700, 64, 2), (200, 300, 128, 2), (300, 300, 256, 2), (200, 300, 96, 2), (600, 700, 192, 2), (1290, 50, 256, 43)])
 def test_masks(torch, nq, nk, D, heads):
     q, k, v = make(torch, nq, nk, heads, 1 if heads == 2 else heads, D, 5)
     for mask in (np.zeros(nk, bool), np.arange(nk) % 2 == 0, np.arange(nk) == nk - 1, np.arange(nk) >= 256,

@@ -355,7 +355,7 @@ def test_accumulators_are_the_kernels_own(assembly):
             assert since >= 19, (name, line, since)
         elif since is not None:
             since += int(line.split()[1]) + 1 if op == "s_nop" else 1
-    assert kernels == 10  # heads of 64, 128 and 256, with and without a mask, 128 (and but for 128) 256 rows to a tile
+    assert kernels == 16  # heads of 64, 96, 128, 192 and 256, with and without a mask, 128 and (64, 192 and 256) 256 rows to a tile
 
 
 def test_host_code_under_asan_and_ubsan(tmp_path):
