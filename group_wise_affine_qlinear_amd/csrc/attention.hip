@@ -142,13 +142,18 @@ struct Division {
   }
   static __device__ __forceinline__ int units_of(const Sample &s) { return max((s.keys + UNIT - 1) / UNIT, 1); }
 
-  // Calls f(Sample, index of lane 0's) with 64 samples at a time, a lane each, until f returns true.
+  // The lane's of the 64 samples from s0 on, an empty one past the last.
+  __device__ __forceinline__ Sample lanes_sample(int s0) const {
+    const int s = s0 + (int)(threadIdx.x & 63);
+    return s < a.samples ? sample_of(a, s) : Sample{0, 0, 0, 0};
+  }
+  // Calls f with 64 samples at a time, a lane each, until it returns true.
   template <typename F> __device__ __forceinline__ void each(F f) {
+    Sample next = mine;
     for (int s0 = 0; s0 < a.samples; s0 += 64) {
-      Sample x = mine;
-      const int s = s0 + (int)(threadIdx.x & 63);
-      if (s0) x = s < a.samples ? sample_of(a, s) : Sample{0, 0, 0, 0};
-      if (f(x, s0)) return;
+      const Sample x = next;
+      next = lanes_sample(s0 + 64);  // on its way meanwhile
+      if (f(x)) return;
     }
   }
   // Pieces of a cut tile.
@@ -172,9 +177,12 @@ struct Division {
       }
       return;
     }
-    const int s = (int)(threadIdx.x & 63);
-    mine = s < a.samples ? sample_of(a, s) : Sample{0, 0, 0, 0};
-    each([&](const Sample &x, int) {
+    mine = lanes_sample(0);
+    if (a.slots == 0 && a.samples > 64) {
+      whole = kMostBlocks;  // nothing is cut: not worth a pass over the offsets to count
+      return;
+    }
+    each([&](const Sample &x) {
       tiles = min(tiles + lane_of(scan(tiles_of(a, x)), 63), kMostBlocks);
       return false;
     });
@@ -182,7 +190,7 @@ struct Division {
     if (whole == tiles) return;
     int first = 0;
     float units = 0.f;  // counted to a few parts in a million
-    each([&](const Sample &x, int) {
+    each([&](const Sample &x) {
       const int n = tiles_of(a, x), incl = scan(n);
       units += lane_of(scan((float)cut_of(first + incl - n, n) * (float)units_of(x)), 63);
       first = min(first + lane_of(incl, 63), kMostBlocks);
@@ -223,7 +231,7 @@ struct Division {
       }
     } else {
       int first = 0, pieces = 0, found = 0;
-      each([&](const Sample &x, int s0) {
+      each([&](const Sample &x) {
         const int n = tiles_of(a, x), incl = scan(n), begin = first + incl - n;
         const int cut = cut_of(begin, n), parts = parts_of(x);
         const int all = (int)min((int64_t)cut * parts, (int64_t)kMostBlocks);
@@ -549,7 +557,7 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
   Division<BQ, UNIT> division(a);
   Work w;
   const int block = blockIdx.x, whole = a.rest_from ? a.rest_from : division.whole;
-  if (!division.find(block < whole ? xcd_order(block, whole) : -1, block - whole, w)) return;
+  if (!division.find(block >= whole ? -1 : whole < kMostBlocks ? xcd_order(block, whole) : block, block - whole, w)) return;
   w = uniform(w);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, h = lane >> 5;
   const int r0 = w.tile * BQ + wave * 32 * NQ;

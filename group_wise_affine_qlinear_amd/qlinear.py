@@ -845,7 +845,7 @@ def qlinear_qk_norm_rope(M, head_dim, *, q=None, k=None, v=None, q_out=None, k_o
     """
     torch = _torch()
     lib = load_library()
-    first = next((t for t in (q, k, v) if t is not None), None)
+    first = q if q is not None else k if k is not None else v
     if not isinstance(first, torch.Tensor):
         raise TypeError("one of q, k and v must be a torch tensor")
     dev = first.device
