@@ -950,44 +950,64 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
 // ------------------------------------------------------------------ joining pieces
 
 // The pieces of the cut tiles become outputs. Grid: x cut tiles, y parts of
-// their work; a thread has one row at a time and 16 of its values.
+// their work; a thread has one row at a time and 4 N of its values: 16, and 4
+// where there are few rows. Mostly latency, for the pieces come from other
+// dies' caches: maxima, sums and values of G pieces are requested together.
+template <int BQ> constexpr int kJoin = BQ == 32 ? 1 : 4;
+
 template <int DP, int BQ, int UNIT>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
+  constexpr int N = kJoin<BQ>, G = N == 1 ? 8 : 4, kSlot = BQ * (DP + 2);
   Division<BQ, UNIT> division(a);
   Work w;
   if (!division.find(division.whole + (int)blockIdx.x, 0, w) || w.slot < 0) return;
   w = uniform(w);
   const int rows = min(w.s.rows - w.tile * BQ, BQ), pieces = w.parts;
   const float *const part = slot_at<DP, BQ>(a, w.slot);
-  constexpr int kSlot = BQ * (DP + 2);
-  for (int n = blockIdx.y * 256 + threadIdx.x; n < rows * (DP / 16); n += 256 * gridDim.y) {
-    const int d16 = (unsigned)n / (unsigned)rows, rt = n - d16 * rows;
-    if (d16 * 16 >= a.D) break;
-    const float *from = part + (d16 * 4 * BQ + rt) * 4, *stats = part + BQ * DP + rt;
+  for (int n = blockIdx.y * 256 + threadIdx.x; n < rows * (DP / (4 * N)); n += 256 * gridDim.y) {
+    const int d4 = (unsigned)n / (unsigned)rows * N, rt = n - d4 / N * rows;
+    if (d4 * 4 >= a.D) break;
+    const float *from = part + (d4 * BQ + rt) * 4, *stats = part + BQ * DP + rt;
     float m = kLowest, sum = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) m = fmaxf(m, stats[(int64_t)i * kSlot]);
-    f32x4 v[4] = {};
-#pragma unroll 2
-    for (int i = 0; i < pieces; ++i) {
-      const int64_t at = (int64_t)i * kSlot;
-      const float f = __builtin_amdgcn_exp2f(stats[at] - m);
-      sum = __builtin_fmaf(stats[at + BQ], f, sum);
+    f32x4 v[N] = {};
+    for (int i0 = 0; i0 < pieces; i0 += G) {
+      float pm[G], pl[G];
+      f32x4 x[G][N];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f32x4 x = *reinterpret_cast<const f32x4 *>(from + at + j * BQ * 4);
+      for (int g = 0; g < G; ++g) {
+        const int64_t at = (int64_t)(i0 + g) * kSlot;
+        const bool in = i0 + g < pieces;
+        pm[g] = in ? stats[at] : kLowest;
+        pl[g] = in ? stats[at + BQ] : 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[j][e] = __builtin_fmaf(x[e], f, v[j][e]);
+        for (int j = 0; j < N; ++j) x[g][j] = in ? *reinterpret_cast<const f32x4 *>(from + at + j * BQ * 4) : f32x4{};
+      }
+      float top = m;
+#pragma unroll
+      for (int g = 0; g < G; ++g) top = fmaxf(top, pm[g]);
+      const float old = __builtin_amdgcn_exp2f(m - top);
+      m = top;
+      sum *= old;
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[j][e] *= old;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float f = __builtin_amdgcn_exp2f(pm[g] - m);
+        sum = __builtin_fmaf(pl[g], f, sum);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[j][e] = __builtin_fmaf(x[g][j][e], f, v[j][e]);
       }
     }
     const float inv = reciprocal(sum);
-    uint16_t *o = out_row(a, w, w.tile * BQ + rt) + d16 * 16;
+    uint16_t *o = out_row(a, w, w.tile * BQ + rt) + d4 * 4;
 #pragma unroll
-    for (int j = 0; j < 4; j += 2)
-      if (d16 * 16 + j * 4 < a.D)
-        *reinterpret_cast<u32x4 *>(o + j * 4) =
-            u32x4{pack_bf16(v[j][0] * inv, v[j][1] * inv), pack_bf16(v[j][2] * inv, v[j][3] * inv),
-                  pack_bf16(v[j + 1][0] * inv, v[j + 1][1] * inv), pack_bf16(v[j + 1][2] * inv, v[j + 1][3] * inv)};
+    for (int j = 0; j < N; ++j)
+      if (d4 * 4 + j * 4 < a.D)
+        *reinterpret_cast<u32x2 *>(o + j * 4) = u32x2{pack_bf16(v[j][0] * inv, v[j][1] * inv), pack_bf16(v[j][2] * inv, v[j][3] * inv)};
   }
 }
 
@@ -996,7 +1016,8 @@ int padded(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : D <= 1
 constexpr int kCus = 256;  // MI355X
 
 // Parts of a cut tile's join: at most 256 threads' work each.
-template <int DP, int BQ> constexpr int kJoinParts = BQ * (DP / 16) > 256 ? BQ * (DP / 16) / 256 : 1;
+template <int DP, int BQ>
+constexpr int kJoinParts = BQ * DP / (4 * kJoin<BQ>) > 256 ? BQ * DP / (4 * kJoin<BQ>) / 256 : 1;
 
 template <int DP, int NQ>
 void launch_rows(const AttentionArgs &a, const AttentionPlan &p, hipStream_t stream) {
