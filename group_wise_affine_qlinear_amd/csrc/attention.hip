@@ -33,7 +33,7 @@ constexpr float kLowest = -3.4028234663852886e38f;
 // then stay below 2^kSlack and the sums far below fp32's limit, and the
 // outputs are rescaled a few times instead of at every tile.
 constexpr float kSlack = 8.f;
-constexpr int kOut = 0x7FFFFFFF;  // an offset past every buffer: the load gives zeros
+constexpr uint32_t kOut = 0x7FFFFFFF;  // an offset past every buffer: the load gives zeros
 
 // 16-byte unit that holds unit c of a row in LDS. K is read 16 bytes per lane
 // by 32 rows at once (units of eight rows in a row of 128 bytes each), V eight
@@ -281,9 +281,9 @@ struct Queries {
   bf16x8 q[NQ][DP / 16];     // Q^T: lane's query, 8 values at 16 i + 8 (lane / 32)
   float m[NQ], l[NQ];        // maximum followed (in powers of two), sum of this half's weights
 };
-template <int DP, int NQ>
-struct State : Queries<DP, NQ> {
-  f32x16 o[NQ][DP / 32];     // O^T
+template <int DP>
+struct State : Queries<DP, 1> {
+  f32x16 o[DP / 32];         // O^T
 };
 
 // Row r of a sample's rows: query r / group, head r % group of the key head's.
@@ -299,108 +299,15 @@ __device__ __forceinline__ void load_q(const AttentionArgs &a, const Work &w, in
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
     const int r = r0 + 32 * i + (lane & 31), m = query_of(a, r);
-    const int at = r < w.s.rows ? (int)((m - m0) * a.q_ld + (r - m * a.group) * a.D + 8 * (lane >> 5)) * 2 : kOut;
+    const uint32_t at = r < w.s.rows ? (uint32_t)((m - m0) * a.q_ld + (r - m * a.group) * a.D + 8 * (lane >> 5)) * 2 : kOut;
 #pragma unroll
     for (int j = 0; j < DP / 16; ++j) {
       const int d = 16 * j + 8 * (lane >> 5);
-      st.q[i][j] = as_bf16x8(__builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, d < a.D ? at + 32 * j : kOut, 0, 0)));
+      st.q[i][j] = as_bf16x8(__builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, (int)(d < a.D ? at + 32 * j : kOut), 0, 0)));
     }
     st.m[i] = kLowest;
     st.l[i] = 0.f;
   }
-}
-
-// S^T of the 32 keys whose K rows are at kb.
-template <int DP, int NQ>
-__device__ __forceinline__ void scores(const unsigned char *kb, const State<DP, NQ> &st, f32x16 (&s)[NQ]) {
-  const int lane = threadIdx.x & 63, row = lane & 31, h = lane >> 5;
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) s[i] = f32x16{};
-  int base[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) base[j] = row * (lds_width(DP) * 2) + k_unit(row, 2 * j + h) * 16;
-#pragma unroll
-  for (int j = 0; j < DP / 16; ++j) {
-    const bf16x8 k = lds_read8(kb + base[j & 3] + (j >> 2) * 128);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) s[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, st.q[i][j], s[i], 0, 0, 0);
-  }
-}
-
-// One tile's scores become weights: keys whose bit in `valid` is clear get
-// none; the maximum, the sum and, where the maximum is followed, the output so
-// far are brought up to date.
-template <int DP, int NQ>
-__device__ __forceinline__ void weights(State<DP, NQ> &st, f32x16 (&s)[NQ], float c, uint32_t valid, bf16x8 (&p)[NQ][2]) {
-  const int h = (threadIdx.x >> 5) & 1;
-  if (valid != 0xFFFFFFFFu) {
-    const uint32_t mine = valid >> (4 * h);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const bool keep = (mine >> acc_row(r)) & 1;
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) s[i][r] = keep ? s[i][r] : -__builtin_inff();
-    }
-  }
-  float mx[NQ];
-  bool follow = false;
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    float x = s[i][0];
-#pragma unroll
-    for (int r = 1; r < 16; ++r) x = fmaxf(x, s[i][r]);
-    mx[i] = fmaxf(x, other_half(x)) * c;
-    follow |= mx[i] > st.m[i] + kSlack;
-  }
-  if (__any(follow)) {
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      // each query by its own scores alone
-      const float m = mx[i] > st.m[i] + kSlack ? mx[i] : st.m[i];
-      const float f = __builtin_amdgcn_exp2f(st.m[i] - m);
-      st.m[i] = m;
-      st.l[i] *= f;
-#pragma unroll
-      for (int j = 0; j < DP / 32; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) st.o[i][j][r] *= f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    uint32_t w[8];
-#pragma unroll
-    for (int r = 0; r < 16; r += 2) {
-      const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][r], c, -st.m[i]));
-      const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][r + 1], c, -st.m[i]));
-      w[r / 2] = pack_bf16(a, b);
-    }
-#pragma unroll
-    for (int r = 0; r < 8; ++r) st.l[i] += bf16_lo(w[r]) + bf16_hi(w[r]);
-    p[i][0] = as_bf16x8(u32x4{w[0], w[1], w[2], w[3]});
-    p[i][1] = as_bf16x8(u32x4{w[4], w[5], w[6], w[7]});
-  }
-}
-
-// O^T += V^T P^T over the 32 V rows at vb.
-template <int DP, int NQ>
-__device__ __forceinline__ void outputs(const unsigned char *vb, State<DP, NQ> &st, const bf16x8 (&p)[NQ][2]) {
-  const int lane = threadIdx.x & 63, h = lane >> 5;
-  const int row = 4 * h + ((lane & 15) >> 2);                         // + 16 t + 8 u
-  const int unit = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1), byte = (lane & 1) * 8;  // + 4 j
-  int base[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) base[j] = row * (lds_width(DP) * 2) + v_unit(row, unit + 4 * j) * 16 + byte;
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int j = 0; j < DP / 32; ++j) {
-      const unsigned char *r = vb + base[j & 1] + (16 * t * lds_width(DP) * 2 + (j >> 1) * 128);
-      const s16x4 lo = lds_read_tr(r), hi = lds_read_tr(r + 8 * lds_width(DP) * 2);
-      const bf16x8 v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) st.o[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[i][t], st.o[i][j], 0, 0, 0);
-    }
 }
 
 // Up to 64 rows of K or V of one key head of a sample, from the sample's key `first` on; what is past them reads as zeros.
@@ -821,6 +728,63 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
 
 // ------------------------------------------------------------------ tiles of few rows
 
+// What a wave of few rows does with 32 keys: S^T of those whose K rows are at kb,
+template <int DP>
+__device__ __forceinline__ f32x16 scores(const Lanes<DP> &at, const unsigned char *kb, const State<DP> &st) {
+  f32x16 s = {};
+#pragma unroll
+  for (int j = 0; j < DP / 16; ++j) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(at.k_frag(kb, j), st.q[0][j], s, 0, 0, 0);
+  return s;
+}
+
+// weights of these scores, none for keys whose bit in `valid` is clear; the
+// maximum, the sum and, where the maximum is followed, the output so far are
+// brought up to date,
+template <int DP>
+__device__ __forceinline__ void weights(State<DP> &st, f32x16 s, float c, uint32_t valid, bf16x8 (&p)[2]) {
+  const int h = (threadIdx.x >> 5) & 1;
+  if (valid != 0xFFFFFFFFu) {
+    const uint32_t mine = valid >> (4 * h);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = (mine >> acc_row(r)) & 1 ? s[r] : -__builtin_inff();
+  }
+  float mx = s[0];
+#pragma unroll
+  for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[r]);
+  mx = fmaxf(mx, other_half(mx)) * c;
+  const bool grown = mx > st.m[0] + kSlack;
+  if (__any(grown)) {
+    // each query by its own scores alone
+    const float m = grown ? mx : st.m[0], f = __builtin_amdgcn_exp2f(st.m[0] - m);
+    st.m[0] = m;
+    st.l[0] *= f;
+#pragma unroll
+    for (int j = 0; j < DP / 32; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) st.o[j][r] *= f;
+  }
+  uint32_t w[8];
+#pragma unroll
+  for (int r = 0; r < 16; r += 2) {
+    const float a = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -st.m[0]));
+    const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r + 1], c, -st.m[0]));
+    w[r / 2] = pack_bf16(a, b);
+  }
+#pragma unroll
+  for (int r = 0; r < 8; ++r) st.l[0] += bf16_lo(w[r]) + bf16_hi(w[r]);
+  p[0] = as_bf16x8(u32x4{w[0], w[1], w[2], w[3]});
+  p[1] = as_bf16x8(u32x4{w[4], w[5], w[6], w[7]});
+}
+
+// and O^T += V^T P^T over the V rows at vb.
+template <int DP>
+__device__ __forceinline__ void outputs(const Lanes<DP> &at, const unsigned char *vb, State<DP> &st, const bf16x8 (&p)[2]) {
+  constexpr int kTiles = DP / 32;
+#pragma unroll
+  for (int f = 0; f < 2 * kTiles; ++f)
+    st.o[f % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(at.v_frag(vb, f), p[f / kTiles], st.o[f % kTiles], 0, 0, 0);
+}
+
 // 32 rows at most: the four waves of a block share them and take every fourth
 // tile of 32 keys each, through LDS of their own, without a barrier until
 // their sums are joined at the end. REST: the rows of a few tiles that the
@@ -845,7 +809,8 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
     w = uniform(w);
   }
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  State<DP, 1> st;
+  State<DP> st;
+  const Lanes<DP> lanes;
   // units are of 64 keys in the kernel above
   const int end = REST ? w.s.keys : min(w.unit1 * UNIT, w.s.keys);
   const float c = __uint_as_float(uniform((int)__float_as_uint(a.scale * 1.4426950408889634f)));
@@ -858,7 +823,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
       const int id = 64 * i + lane, row = id / kUnits;
       const int u = is_k ? k_unit(row, id % kUnits) : v_unit(row, id % kUnits);
       const bool in = u * 8 < a.D && (!MASKED || (keep >> row & 1));
-      dma16(r, in ? (int)(row * ld + u * 8) * 2 : kOut, 0, to + i * 1024);
+      dma16(r, in ? (uint32_t)(row * ld + u * 8) * 2 : kOut, 0, to + i * 1024);
     }
   };
   int at = REST ? 32 * wave : w.unit0 * UNIT + 32 * wave;
@@ -874,26 +839,25 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
   }
   load_q<DP, 1>(a, w, w.tile * BQ, st);
 #pragma unroll
-  for (int j = 0; j < DP / 32; ++j) st.o[0][j] = f32x16{};
+  for (int j = 0; j < DP / 32; ++j) st.o[j] = f32x16{};
   if (at < end) {
     copy(a.v, a.v_ld, false, vb, at, keep);
     for (; at < end; at += 128) {
       // K of the next tile is requested behind this one's scores and V behind its outputs, always, so that what
       // has landed can be counted
       const uint32_t keep_next = (uint32_t)kept<MASKED>(a, w, at + 128, byte_next);
-      f32x16 s[1];
-      bf16x8 p[1][2];
+      bf16x8 p[2];
       __builtin_amdgcn_s_waitcnt((kCopies & 0xF) | ((kCopies >> 4) << 14) | 0xF70);  // all but V
       asm volatile("" ::: "memory");
-      scores<DP, 1>(kb, st, s);
+      const f32x16 s = scores(lanes, kb, st);
       // the reads of K are back before its place is filled again
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if constexpr (MASKED) byte_next = mask_byte(a, w, at + 256);
       copy(a.k, a.k_ld, true, kb, at + 128, keep_next);
-      weights<DP, 1>(st, s, c, keep, p);
+      weights(st, s, c, keep, p);
       __builtin_amdgcn_s_waitcnt((kCopies & 0xF) | ((kCopies >> 4) << 14) | 0xF70);  // all but the next K
       asm volatile("" ::: "memory");
-      outputs<DP, 1>(vb, st, p);
+      outputs(lanes, vb, st, p);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       copy(a.v, a.v_ld, false, vb, at + 128, keep_next);
       keep = keep_next;
@@ -909,7 +873,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
 #pragma unroll
     for (int g = 0; g < 4; ++g)
       to[(8 * (j % kTiles) + 2 * g + h) * 32 + col] =
-          f32x4{st.o[0][j][4 * g], st.o[0][j][4 * g + 1], st.o[0][j][4 * g + 2], st.o[0][j][4 * g + 3]};
+          f32x4{st.o[j][4 * g], st.o[j][4 * g + 1], st.o[j][4 * g + 2], st.o[j][4 * g + 3]};
   }
   if (h == 0) {
     ms[wave][col] = st.m[0];
