@@ -1170,7 +1170,7 @@ QL_API int qlinear_attention(const ql_attention_args *a, void *stream) {
   const int64_t samples = a->q_offsets ? a->samples : 1;
   const int st = attention_sizes(a->Mq, a->Mk, samples, a->q_heads, a->kv_heads, a->head_dim);
   if (st != QL_OK) return st;
-  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return QL_EINVAL;
+  if (!(a->scale >= 1e-30f && a->scale <= 1e30f)) return QL_EINVAL;  // log2(e) of it is fp32 then
   if (a->Mq == 0 || samples == 0) return QL_OK;
   if (!a->q || !a->out || (a->Mk > 0 && (!a->k || !a->v))) return QL_EINVAL;
   const int64_t q_row = a->q_heads * a->head_dim, kv_row = a->kv_heads * a->head_dim;

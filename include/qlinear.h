@@ -642,7 +642,7 @@ typedef struct ql_attention_args {
   int64_t Mq, Mk;              /* rows; Mq * q_heads / kv_heads and Mk up to 2^30 */
   int64_t q_heads, kv_heads;   /* q_heads a multiple of kv_heads: query head h reads key head h * kv_heads / q_heads */
   int64_t head_dim;            /* D, a multiple of 8, 8 .. 256                  */
-  float scale;                 /* > 0, finite; usually 1 / sqrt(D)              */
+  float scale;                 /* 1e-30 .. 1e30; usually 1 / sqrt(D)            */
   int64_t samples;             /* with offsets, up to 2^20                      */
   const int32_t *q_offsets;    /* int32 [samples + 1]: sample s has the queries [q_offsets[s], q_offsets[s+1]), */
   const int32_t *k_offsets;    /* and the keys [k_offsets[s], k_offsets[s+1]); both, or both NULL: one sample */

@@ -114,7 +114,8 @@ SIZES = [
     (128, 128, 2, 2, 256), (7, 700, 6, 2, 136), (300, 1, 2, 2, 128), (257, 321, 2, 2, 128), (513, 200, 1, 1, 256),
     # tiles behind as many as the card holds, which go 32 rows to a block
     (2500, 70, 26, 26, 128), (1290, 40, 43, 43, 256),
-    (260, 515, 2, 1, 96), (400, 700, 2, 2, 192), (130, 300, 2, 1, 160), (9, 3000, 4, 2, 176), (700, 400, 20, 20, 184), (33, 1500, 2, 2, 88), (1, 5000, 4, 4, 256), (3, 9001, 8, 1, 64), (140, 3001, 2, 1, 256), (300, 2049, 1, 1, 64),
+    (260, 515, 2, 1, 96), (400, 700, 2, 2, 192), (130, 300, 2, 1, 160), (9, 3000, 4, 2, 176), (700, 400, 20, 20, 184),
+    (33, 1500, 2, 2, 88), (1, 5000, 4, 4, 256), (3, 9001, 8, 1, 64), (140, 3001, 2, 1, 256), (300, 2049, 1, 1, 64),
 ]
 
 
@@ -155,7 +156,39 @@ def test_ragged(torch, q_len, k_len, hq, hkv, D, masked):
     check(torch, q, k, v, q_len, k_len, mask, first=(4, 5))
 
 
-@pytest.mark.parametrize("nq,nk,D,heads", [(3, 700, 64, 2), (200, 300, 128, 2), (300, 300, 256, 2), (200, 300, 96, 2), (600, 700, 192, 2), (1290, 50, 256, 43)])
+MANY = [
+    # samples, queries of each, keys of each: more samples than a wave has lanes, whose keys are cut into pieces
+    (65, lambda i: 1 + i % 3, lambda i: 400 + 97 * i % 3000, 2, 1, 64),
+    (131, lambda i: i % 2, lambda i: 1500 + 211 * i % 1000, 1, 1, 128),
+    (67, lambda i: 1 + 5 * i % 90, lambda i: 100 + 61 * i % 1200, 1, 1, 72),
+    (66, lambda i: 40 if i != 64 else 700, lambda i: 330 + 61 * i % 900, 2, 2, 256),
+    (64, lambda i: 40, lambda i: 0 if i % 3 else 1900, 2, 2, 128),
+]
+
+
+@pytest.mark.parametrize("samples,q_of,k_of,hq,hkv,D", MANY)
+@pytest.mark.parametrize("workspace", [ql.TORCH_WORKSPACE, None])
+def test_many_samples(torch, samples, q_of, k_of, hq, hkv, D, workspace):
+    q_len, k_len = [q_of(i) for i in range(samples)], [k_of(i) for i in range(samples)]
+    q, k, v = make(torch, sum(q_len) + 6, sum(k_len) + 5, hq, hkv, D, samples)
+    assert ql.qlinear_attention_workspace_bytes(q.shape[0], k.shape[0], samples, hq, hkv, D) > 0
+    check(torch, q, k, v, q_len, k_len, first=(3, 2), workspace=workspace)
+
+
+@pytest.mark.parametrize("nq,nk,hq,hkv,D", [(3, 4000, 4, 2, 64), (100, 3000, 2, 2, 128), (300, 3000, 2, 1, 256),
+                                            (1290, 40, 43, 43, 256)])
+def test_in_place(torch, nq, nk, hq, hkv, D):
+    """out is q, also where a tile's keys are cut or its rows go 32 to a block."""
+    q, k, v = make(torch, nq, nk, hq, hkv, D, 53)
+    want = ql.qlinear_attention(q, k, v, torch.empty_like(q))
+    for workspace in (ql.TORCH_WORKSPACE, None):
+        again = q.clone()
+        check(torch, again, k, v, workspace=workspace, out=again)
+        assert workspace is None or torch.equal(again, want)
+
+
+@pytest.mark.parametrize("nq,nk,D,heads", [(3, 700, 64, 2), (200, 300, 128, 2), (300, 300, 256, 2), (200, 300, 96, 2),
+                                           (600, 700, 192, 2), (1290, 50, 256, 43)])
 def test_masks(torch, nq, nk, D, heads):
     q, k, v = make(torch, nq, nk, heads, 1 if heads == 2 else heads, D, 5)
     for mask in (np.zeros(nk, bool), np.arange(nk) % 2 == 0, np.arange(nk) == nk - 1, np.arange(nk) >= 256,
@@ -190,6 +223,14 @@ def test_wide_scores(torch, nq, nk, D):
     check(torch, q, k, v)
     check(torch, q, k.flip(0).contiguous(), v, scale=0.5)
     check(torch, q, k, v, scale=1e-6)
+    # the least of scales hides no key more and none less; the largest leaves the best key's value
+    mask = np.arange(nk) % 3 != 0
+    check(torch, q, k, v, scale=1e-30, mask=mask)
+    q, k = torch.ones_like(q), -torch.ones_like(k)
+    k[nk // 2] = 1.0
+    out = torch.empty_like(q)
+    ql.qlinear_attention(q, k, v, out, scale=1e30)
+    assert torch.equal(out, v[nk // 2].expand_as(out))
 
 
 @pytest.mark.parametrize("nq", [2, 40, 300])
@@ -398,3 +439,30 @@ def test_run_from_projection_to_projection(torch):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(stream, eager)
+
+
+def test_two_graphs_share_a_workspace(torch):
+    """Nothing in a workspace is kept: graphs that share one may be replayed in any order, one after the other."""
+    a, b = make(torch, 2, 3000, 2, 1, 128, 59), make(torch, 300, 1500, 2, 2, 256, 61)
+    need = [ql.qlinear_attention_workspace_bytes(q.shape[0], k.shape[0], 1, q.shape[1], k.shape[1], q.shape[2])
+            for q, k, _ in (a, b)]
+    assert min(need) > 0
+    ws = torch.empty(max(need), dtype=torch.uint8, device="cuda")
+    want = [check(torch, *x) for x in (a, b)]
+    outs = [torch.zeros_like(x[0]) for x in (a, b)]
+    graphs = []
+    for x, o in zip((a, b), outs):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            ql.qlinear_attention(*x, o, workspace=ws)
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1)):
+        for o in outs:
+            o.zero_()
+        for i in order:
+            graphs[i].replay()
+        ws.fill_(255)  # eager work between the replays
+        torch.cuda.synchronize()
+        for i in set(order):
+            assert torch.equal(outs[i], want[i])

@@ -151,6 +151,8 @@ def _att(**kw):
     (dict(scale=-1.0), ql.QL_EINVAL),
     (dict(scale=float("nan")), ql.QL_EINVAL),
     (dict(scale=float("inf")), ql.QL_EINVAL),
+    (dict(scale=1.1e30), ql.QL_EINVAL),
+    (dict(scale=0.9e-30), ql.QL_EINVAL),
     (dict(q_offsets=0), ql.QL_EINVAL),
     (dict(k_offsets=0), ql.QL_EINVAL),
     (dict(q=0), ql.QL_EINVAL),
