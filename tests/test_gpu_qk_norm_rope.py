@@ -121,6 +121,35 @@ def test_pitches(torch, layout, dtype, extra):
     check(torch, 41, 4, 2, 64, dtype=dtype, layout=layout, extra=extra)
 
 
+@pytest.mark.parametrize("what", ["q", "q_out", "q_weight", "k_weight", "small"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["halves", "pairs"])
+def test_arrays_aligned_to_their_elements_only(torch, layout, dtype, what):
+    """One array one element behind an aligned address gives the same bits; tables and positions may always be such."""
+    M, D = 21, 72
+    q, k, v, g = make(torch, M, 3, 2, D, torch.float32 if dtype == "f32" else torch.bfloat16, 13)
+    freqs, axis, pos = tables(torch, g, 20, 2, M, 0)
+    w = {n: (1 + 0.3 * torch.randn(D, generator=g)).cuda() for n in ("q_weight", "k_weight")}
+
+    def behind(t):
+        moved = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+        return moved.copy_(t)
+
+    def call(q, q_out, freqs, axis, pos, weights):
+        outs = [torch.empty((M, n, D), dtype=torch.bfloat16, device="cuda") for n in (2, 2)]
+        ql.qlinear_qk_norm_rope(M, D, q=q, k=k, v=v, q_out=q_out, k_out=outs[0], v_out=outs[1], norm=KIND["rms"],
+                                rope=LAYOUT[layout], freqs=freqs, pair_axis=axis, positions=pos, **weights)
+        return [q_out] + outs
+
+    out = lambda: torch.zeros((M, 3, D), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    want = call(q, out(), freqs, axis, pos, w)
+    small = behind if what == "small" else lambda t: t  # noqa: E731
+    got = call(behind(q) if what == "q" else q, behind(out()) if what == "q_out" else out(), small(freqs), small(axis),
+               small(pos), {n: behind(t) if what == n else t for n, t in w.items()})
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("far", [1 << 20, 16000000, -16000000])
 def test_far_positions(torch, far):
     check(torch, 33, 2, 1, 128, dtype="f32", far=far)
