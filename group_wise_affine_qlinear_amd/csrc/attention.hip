@@ -13,9 +13,14 @@
 // comes from LDS by transposing reads, so no operand crosses lanes.
 //
 // Scores, maxima, sums and outputs are fp32; P enters the second product as
-// bf16 (its operand type, error 2^-9 of a weight), and the sum is taken of the
-// rounded weights, so that what the output is divided by is exactly what it
-// was multiplied by. The output is rounded once.
+// bf16 (its operand type, error up to 2^-8 of a weight), and the sum is taken
+// of the rounded weights, so that what the output is divided by is exactly what
+// it was multiplied by. The output is rounded once.
+//
+// Three kernels: attention_kernel for tiles of 128 or 256 rows, bound by the
+// matrix unit; attention_few_kernel for up to 32, bound by the bytes of K and V
+// or, on few CUs, by their latency; attention_join_kernel for tiles whose keys
+// were cut into pieces to fill the card. attention_plan() chooses.
 #include <algorithm>
 #include <utility>
 
@@ -31,13 +36,17 @@ typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 constexpr float kLowest = -3.4028234663852886e38f;
 // A maximum is followed only when it has grown by more than 2^kSlack: weights
 // then stay below 2^kSlack and the sums far below fp32's limit, and the
-// outputs are rescaled a few times instead of at every tile.
+// outputs are rescaled a few times instead of every 32 keys (which would take
+// as many instructions of the vector unit as the weights themselves).
 constexpr float kSlack = 8.f;
 constexpr uint32_t kOut = 0x7FFFFFFF;  // an offset past every buffer: the load gives zeros
 
-// 16-byte unit that holds unit c of a row in LDS. K is read 16 bytes per lane
-// by 32 rows at once (units of eight rows in a row of 128 bytes each), V eight
-// bytes per lane from four rows (two units of each).
+// 16-byte unit that holds unit c of a row in LDS. K is read 16 bytes per lane,
+// the same unit of 32 rows at once: eight rows in turn have theirs at eight
+// different places of 128 bytes. V is read eight bytes per lane, two units of
+// four rows at once, which lie side by side in 128 bytes. Over twice as many
+// places neither is faster (4608 tokens of 18 heads of 256: V 379 us against
+// 380, K 383).
 __device__ __forceinline__ int k_unit(int row, int c) { return c ^ (row & 7); }
 __device__ __forceinline__ int v_unit(int row, int c) { return c ^ ((row & 3) * 2); }
 
@@ -400,7 +409,7 @@ struct Lanes {
 
 template <int TILES>
 struct Acc {
-  // Waits before an accumulator is read or written by anything but a product (a product takes 16 passes).
+  // Waits before an accumulator is read or written by anything but a product: 24 states, more than any product asks for.
   static __device__ __forceinline__ void settle() { QL_ACC_ASM(TILES, "s_nop 15\n\ts_nop 7" : :); }
 
   // Tile N += a b. The wait covers an operand that a VALU instruction wrote just before.
@@ -454,6 +463,18 @@ __device__ __forceinline__ void constants(F f) { constants(std::make_integer_seq
 //
 // While the scores of chunk i + 1 are multiplied, those of chunk i become
 // weights between the MFMAs; while these meet V, the next maximum is taken.
+//
+// 4 D multiply-adds per row and key are two MFMAs of 32 cycles for 16 KB of
+// operands, so the matrix unit bounds it, and the card's power with it: 16896
+// tokens of 18 heads of 256 take 4.3 to 4.7 ms (1110 to 1220 TFLOP/s) with the
+// unit busy in 54 % of the cycles of a clock that falls to 2.0 GHz; without the
+// exponentials the loop reaches 1099 TFLOP/s where it was at 1051, without the
+// softmax 1243, with the MFMAs alone 1315; a library product of 8192^3 1200 to
+// 1340. 4608 tokens: 361 to 376 us, 18 of them the join of the last tiles.
+// 64 rows per wave (NQ = 2) read LDS half as often for the same products; with
+// 32 and without the order below the large call took 7.6 ms. Copies go from
+// memory to LDS without registers, and two chunks ahead: all but the newest
+// batch are waited for, never all.
 template <int DP, int NQ, bool MASKED>
 __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
   constexpr int kRow = lds_width(DP) * 2, BQ = 128 * NQ, UNIT = 64, kBytes = UNIT * kRow, kHalf = kBytes / 2;
@@ -789,6 +810,11 @@ __device__ __forceinline__ void outputs(const Lanes<DP> &at, const unsigned char
 // tile of 32 keys each, through LDS of their own, without a barrier until
 // their sums are joined at the end. REST: the rows of a few tiles that the
 // kernel above left, 32 to a block.
+//
+// Bound by the bytes of K and V where many blocks run (16 queries over 65536
+// keys of 8 heads of 128: 56 us, 4.8 TB/s, and 6 for the join), and by what one
+// CU has on its way where few do: 128 KB of LDS, so 18 blocks of one query over
+// 512 keys of 256 (512 KB each) take 12 us of which 3.4 are the launch.
 template <int DP, bool MASKED, bool REST>
 __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) {
   constexpr int kRow = lds_width(DP) * 2, BQ = 32, UNIT = 128, kBytes = 32 * kRow, kUnits = kRow / 16;
@@ -916,7 +942,9 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
 // The pieces of the cut tiles become outputs. Grid: x cut tiles, y parts of
 // their work; a thread has one row at a time and 4 N of its values: 16, and 4
 // where there are few rows. Mostly latency, for the pieces come from other
-// dies' caches: maxima, sums and values of G pieces are requested together.
+// dies' caches: maxima, sums and values of G pieces are requested together
+// (512 pieces of 32 rows of 128 values 5.8 us, one at a time 9.0). Pieces of
+// 256 rows are bytes: 68 MB of them 19 us, 3.5 TB/s.
 template <int BQ> constexpr int kJoin = BQ == 32 ? 1 : 4;
 
 template <int DP, int BQ, int UNIT>

@@ -12,8 +12,14 @@
 // A head lies on the power of two of lanes that holds 8 values each, so a
 // wave works on 64 / lanes heads at once, every value is read once and written
 // once and the sums of a norm are DPP moves. The angles depend on the row
-// alone: the threads of a block make each cosine and sine of its rows once and
-// all heads are turned by them from LDS.
+// alone: the threads of a block make each cosine and sine of its row once and
+// all heads are turned by them from LDS (made per head and lane, 2047 rows of
+// 48 heads of 128 took 19 us instead of 12.4).
+//
+// Bound by its bytes: 16896 rows of 54 heads of 256 (fp32 in, bf16 out, 1.4 GB)
+// 261 us, 5.4 TB/s, as a large copy; 4608 rows 75 us, 5.1 TB/s; 2047 text rows
+// (50 MB) 12.4 us in a graph, of which 3 are the launch and a row's first loads
+// and angles most of the rest. One row takes 3.4 us, the launch.
 #include "ql_block.h"
 #include "ql_kernels.h"
 
