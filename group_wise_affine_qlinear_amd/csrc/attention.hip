@@ -88,10 +88,16 @@ __device__ __forceinline__ Sample sample_of(const AttentionArgs &a, int s) {
   return r;
 }
 
-// Sums over the lanes up to and with this one.
-template <typename T>
-__device__ __forceinline__ T scan(T v) {
-  auto add = [&](auto moved) { v += __builtin_bit_cast(T, moved); };
+struct Plus {
+  template <typename T> __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+struct Most {
+  template <typename T> __device__ __forceinline__ T operator()(T a, T b) const { return max(a, b); }
+};
+// Sums (or maxima of what is not negative) over the lanes up to and with this one.
+template <typename T, typename Op = Plus>
+__device__ __forceinline__ T scan(T v, Op op = {}) {
+  auto add = [&](auto moved) { v = op(v, __builtin_bit_cast(T, moved)); };
   const auto bits = [&] { return __builtin_bit_cast(int, v); };
   add(__builtin_amdgcn_update_dpp(0, bits(), 0x111, 0xF, 0xF, true));   // row_shr:1
   add(__builtin_amdgcn_update_dpp(0, bits(), 0x112, 0xF, 0xF, true));   // row_shr:2
@@ -135,17 +141,65 @@ __device__ __forceinline__ Work uniform(const Work &w) {
 
 // The division of a call's tiles over blocks: which sample, head, rows and
 // keys a block has. The first `whole` tiles belong to a block each; the keys
-// of the others are cut into pieces of `per` units, so that about a.slots
-// pieces come out. All of it follows from the offsets, so every wave of every
-// block finds the same.
+// of the others are cut into pieces of `per` units, so that about as many
+// pieces come out as blocks run at once (a.slots), or twice as many. All of it
+// follows from the offsets, so every wave of every block finds the same.
 constexpr int kMostBlocks = 1 << 24;  // of a call that is served
+
+// Tiles of few rows are all cut, of many rows those behind the last whole round
+// of blocks; into pieces of this many units at least.
+__host__ __device__ constexpr bool cuts_all(int rows) { return rows == 32; }
+__host__ __device__ constexpr int least_units(int rows) { return rows == 32 ? 2 : 3; }
+
+// a / b of whole numbers, rounded down; of more than 2^20 it may be off by some. (Every block of every call with
+// offsets divides a dozen times before its first load: 1 to 2 us where all digits are taken.)
+__host__ __device__ __forceinline__ int quotient(int a, int b) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const float inverse = __builtin_amdgcn_rcpf((float)b);
+#else
+  const float inverse = 1.f / (float)b;
+#endif
+  return (int)((float)a * inverse + 1e-4f);
+}
+
+// Units of a piece where `cut` tiles of `units` units each are cut so that
+// pieces come out for `blocks` blocks, as many of every tile.
+__host__ __device__ __forceinline__ int equal_pieces(int units, int cut, int blocks, int least_units) {
+  const int by_blocks = quotient(blocks, cut), by_units = units / least_units;
+  const int most = by_blocks < by_units ? by_blocks : by_units;
+  return most > 1 ? quotient(units + most - 1, most) : units;
+}
+// Tiles of many rows are cut into pieces for one round of blocks or for two
+// (144 tiles in 256 blocks leave 112 idle in one round, three pieces of each
+// fill two), whichever is over first, or not at all. A round takes the units of
+// a piece; whole tiles 2 more (outputs); the partial sums of a round of pieces
+// go out and come back in 8 units' time, and the launch that joins them takes 4.
+// Heads of 256, 256 rows to a tile, not cut and in two rounds: 162 tiles of 36
+// units 113 and 149 us, 144 of 64 195 and 189, 164 of 264 behind 1024 whole ones
+// 4.53 and 4.23 ms; 104 of 19 behind 256, not cut and in one round: 154 and 141.
+// Heads of 128, 256 tiles of 16 units for 512 blocks: not cut 26, cut 37.
+// mean, longest: units of the cut tiles. Returns the units of a piece, `longest` if none is to be cut.
+__host__ __device__ __forceinline__ int best_length(int mean, int longest, int cut, int slots, int one, int two) {
+  const auto cost = [&](int length) {
+    if (length >= longest) return longest + 2;
+    const int pieces = quotient(mean + length - 1, length) * cut;
+    return quotient(pieces + slots - 1, slots) * length + 4 + quotient(8 * pieces, slots);
+  };
+  const int best = cost(two) < cost(one) ? two : one;
+  return cost(best) < longest + 2 ? best : longest;
+}
 
 template <int BQ, int UNIT>
 struct Division {
   const AttentionArgs &a;
   Sample mine;  // the lane's of the first 64 samples
   int tiles = 0, whole = 0, per = 1 << 30;
+  static constexpr bool kAll = cuts_all(BQ);
+  static constexpr int kLeast = least_units(BQ);
 
+  __device__ __forceinline__ int whole_of(int tiles) const {
+    return a.slots == 0 ? tiles : kAll ? 0 : (int)((unsigned)tiles / (unsigned)a.slots) * a.slots;
+  }
   static __device__ __forceinline__ int tiles_of(const AttentionArgs &a, const Sample &s) {
     return (s.rows + BQ - 1) / BQ * a.kv_heads;
   }
@@ -177,13 +231,16 @@ struct Division {
     if (a.samples == 1) {
       mine = sample_of(a, 0);
       tiles = tiles_of(a, mine);
-      whole = a.slots == 0 ? tiles : a.cut_all ? 0 : (int)((unsigned)tiles / (unsigned)a.slots) * a.slots;
-      // as many pieces of every tile as there are blocks for
-      const int cut = tiles - whole, units = units_of(mine);
-      if (cut > 0) {
-        const int most = max(min((int)((unsigned)a.slots / (unsigned)cut), units / a.least_units), 1);
-        per = (units + most - 1) / most;
+      if (!a.q_offsets) {
+        whole = a.whole;
+        per = a.per;
+        return;
       }
+      whole = whole_of(tiles);
+      const int cut = tiles - whole, units = units_of(mine);
+      if (cut == 0) return;
+      per = equal_pieces(units, cut, a.slots, kLeast);
+      if (!kAll) per = best_length(units, units, cut, a.slots, per, equal_pieces(units, cut, 2 * a.slots, kLeast));
       return;
     }
     mine = lanes_sample(0);
@@ -195,19 +252,28 @@ struct Division {
       tiles = min(tiles + lane_of(scan(tiles_of(a, x)), 63), kMostBlocks);
       return false;
     });
-    whole = a.slots == 0 ? tiles : a.cut_all ? 0 : (int)((unsigned)tiles / (unsigned)a.slots) * a.slots;
+    whole = whole_of(tiles);
     if (whole == tiles) return;
-    int first = 0;
+    int first = 0, longest = 1;
     float units = 0.f;  // counted to a few parts in a million
     each([&](const Sample &x) {
       const int n = tiles_of(a, x), incl = scan(n);
-      units += lane_of(scan((float)cut_of(first + incl - n, n) * (float)units_of(x)), 63);
+      const int cut = cut_of(first + incl - n, n);
+      units += lane_of(scan((float)cut * (float)units_of(x)), 63);
+      if (!kAll) longest = max(longest, lane_of(scan(cut > 0 ? units_of(x) : 0, Most{}), 63));
       first = min(first + lane_of(incl, 63), kMostBlocks);
       return false;
     });
     // half a piece of every tile is empty on average
     const int cut = tiles - whole;
-    per = max((int)min(units / (float)max(a.slots - cut / 2, a.slots / 2) + 1.f, 1e9f), a.least_units);
+    const auto length = [&](int blocks) {
+      return max((int)min(units * __builtin_amdgcn_rcpf((float)max(blocks - cut / 2, blocks / 2)) + 1.f, 1e9f), kLeast);
+    };
+    per = length(a.slots);
+    if (!kAll) {
+      const int mean = (int)min(units * __builtin_amdgcn_rcpf((float)cut) + 1.f, 1e9f);
+      per = best_length(mean, longest, cut, a.slots, per, length(2 * a.slots));
+    }
   }
 
   __device__ __forceinline__ void set(Work &w, int in, int piece, int parts) const {
@@ -1076,15 +1142,15 @@ AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, bool offse
   // keys 11 and 13 us, 1024 keys 17 and 15, 4096 keys 50 and 21; of 64: 1024
   // keys 7.9 and 9.2, 4096 keys 21 and 11. 256 rows of 16 heads of 256: 300
   // keys 18 and 22, 1000 keys 41 and 25.
-  p.cut_all = p.rows == 32;
-  p.least_units = p.cut_all ? 2 : 3;
-  p.cut_units = !p.cut_all ? 10 : dp > 128 ? 8 : 16;
-  p.slots = workspace ? (p.cut_all ? std::max(at_once, 2 * kCus) : at_once) : 0;
+  const bool all = cuts_all(p.rows);
+  const int least = least_units(p.rows), unit = all ? 128 : 64;
+  p.cut_units = !all ? 10 : dp > 128 ? 8 : 16;
+  p.slots = workspace ? (all ? std::max(at_once, 2 * kCus) : at_once) : 0;
   // Nor are tiles cut that fill the blocks several times over, or where a
   // sample's keys are far below that on average (a batch of which one sample
   // has most of the keys loses by that).
-  const int64_t cut_keys = (p.cut_all ? 128 : 64) * (int64_t)p.cut_units;
-  if (Mk < cut_keys || keys * 2 < cut_keys || (p.cut_all && tiles >= 4 * (int64_t)p.slots)) p.slots = 0;
+  const int64_t cut_keys = (int64_t)unit * p.cut_units;
+  if (Mk < cut_keys || keys * 2 < cut_keys || (all && tiles >= 4 * (int64_t)p.slots)) p.slots = 0;
   // The last tiles of one sample over few keys: 32 rows to a block (8 of a
   // tile) need no second launch to join them and fill the card where cutting
   // the keys does not: 4096 rows of 18 heads of 256 over 512 keys (32 tiles
@@ -1095,8 +1161,20 @@ AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, bool offse
     p.rest_from = (int)(tiles - behind);
     p.slots = 0;
   }
-  if (p.slots > 0) p.cut = p.cut_all ? tiles : offsets ? std::min<int64_t>(tiles, p.slots - 1) : tiles % p.slots;
-  p.pieces = p.cut == 0 ? 0 : p.slots + p.cut;
+  if (p.slots > 0) p.cut = all ? tiles : offsets ? std::min<int64_t>(tiles, p.slots - 1) : tiles % p.slots;
+  p.per = 1 << 30;
+  if (p.cut > 0) {
+    // about the slots, or two rounds of them, and one of each tile more; without offsets all of it is known
+    p.pieces = all ? p.slots + p.cut : 2 * p.slots + p.cut;
+    if (!offsets) {
+      const int units = (int)((Mk + unit - 1) / unit), cut = (int)p.cut;
+      p.per = equal_pieces(units, cut, p.slots, least);
+      if (!all) p.per = best_length(units, units, cut, p.slots, p.per, equal_pieces(units, cut, 2 * p.slots, least));
+      if (p.per == units) p.slots = 0, p.cut = 0;
+      p.pieces = p.cut * ((units + p.per - 1) / p.per);
+    }
+  }
+  p.whole = (int)(tiles - p.cut);
   p.blocks = tiles - p.rest + p.pieces;
   p.partial_bytes = (size_t)p.pieces * p.rows * (dp + 2) * sizeof(float);
   return p;
@@ -1105,10 +1183,10 @@ AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, bool offse
 hipError_t launch_attention(const AttentionArgs &args, const AttentionPlan &p, hipStream_t stream) {
   AttentionArgs a = args;
   a.slots = p.slots;
-  a.cut_all = p.cut_all;
-  a.least_units = p.least_units;
   a.cut_units = p.cut_units;
   a.pieces = p.pieces;
+  a.whole = p.whole;
+  a.per = p.per;
   a.rest_from = p.rest_from;
   switch (padded(a.D)) {
     case 64: launch_width<64>(a, p, stream); break;

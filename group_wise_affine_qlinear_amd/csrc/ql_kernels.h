@@ -233,7 +233,8 @@ struct AttentionArgs {
   const uint8_t *key_mask;               // or null
   float *partial;                        // workspace
   // set by launch_attention from the plan
-  int slots, cut_all, least_units, cut_units;
+  int slots, cut_units;
+  int whole, per;                        // without offsets
   int rest_from;
   int64_t pieces;
 };
@@ -241,9 +242,8 @@ struct AttentionArgs {
 struct AttentionPlan {
   int rows;              // query rows of a tile: 32, 128 or 256
   int slots;             // blocks that the keys of cut tiles are divided over; 0: none is cut
-  int cut_all;           // 1: all tiles, 0: those behind the last multiple of slots
-  int least_units;       // units of keys of a piece at least, where a sample has enough
   int cut_units;         // units of keys from which a tile is cut
+  int whole, per;        // without offsets: the tiles before the cut ones, and units of a piece
   int64_t cut, pieces;   // cut tiles and their pieces at most
   int64_t rest;          // last tiles that go 32 rows to a block instead, from tile rest_from on
   int rest_from;

@@ -163,6 +163,9 @@ MANY = [
     (67, lambda i: 1 + 5 * i % 90, lambda i: 100 + 61 * i % 1200, 1, 1, 72),
     (66, lambda i: 40 if i != 64 else 700, lambda i: 330 + 61 * i % 900, 2, 2, 256),
     (64, lambda i: 40, lambda i: 0 if i % 3 else 1900, 2, 2, 128),
+    # one long sample among short ones; two rounds of pieces
+    (5, lambda i: 200, lambda i: 6000 if i == 2 else 70, 4, 4, 64),
+    (2, lambda i: 260, lambda i: 1500 - 41 * i, 40, 40, 256),
 ]
 
 
