@@ -532,11 +532,11 @@ __device__ __forceinline__ void constants(F f) { constants(std::make_integer_seq
 //
 // 4 D multiply-adds per row and key are two MFMAs of 32 cycles for 16 KB of
 // operands, so the matrix unit bounds it, and the card's power with it: 16896
-// tokens of 18 heads of 256 take 4.3 to 4.7 ms (1110 to 1220 TFLOP/s) with the
+// tokens of 18 heads of 256 take 4.2 to 4.5 ms (1170 to 1240 TFLOP/s) with the
 // unit busy in 54 % of the cycles of a clock that falls to 2.0 GHz; without the
 // exponentials the loop reaches 1099 TFLOP/s where it was at 1051, without the
 // softmax 1243, with the MFMAs alone 1315; a library product of 8192^3 1200 to
-// 1340. 4608 tokens: 361 to 376 us, 18 of them the join of the last tiles.
+// 1340. 4608 tokens: 361 to 376 us, 19 of them the join of the last tiles.
 // 64 rows per wave (NQ = 2) read LDS half as often for the same products; with
 // 32 and without the order below the large call took 7.6 ms. Copies go from
 // memory to LDS without registers, and two chunks ahead: all but the newest
@@ -1010,7 +1010,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
 // where there are few rows. Mostly latency, for the pieces come from other
 // dies' caches: maxima, sums and values of G pieces are requested together
 // (512 pieces of 32 rows of 128 values 5.8 us, one at a time 9.0). Pieces of
-// 256 rows are bytes: 68 MB of them 19 us, 3.5 TB/s.
+// 256 rows are bytes: 492 of them, 130 MB, 35 us, 3.7 TB/s.
 template <int BQ> constexpr int kJoin = BQ == 32 ? 1 : 4;
 
 template <int DP, int BQ, int UNIT>
@@ -1175,7 +1175,7 @@ AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, bool offse
     }
   }
   p.whole = (int)(tiles - p.cut);
-  p.blocks = tiles - p.rest + p.pieces;
+  p.blocks = (offsets ? tiles : p.whole) - p.rest + p.pieces;
   p.partial_bytes = (size_t)p.pieces * p.rows * (dp + 2) * sizeof(float);
   return p;
 }
