@@ -1053,12 +1053,12 @@ QL_API int qlinear_qk_norm_rope(const ql_qk_args *a, void *stream) {
       a->pairs % 4 || a->axes > kMaxHeads)
     return QL_EUNSUPPORTED;
   if (a->pairs > a->head_dim / 2) return QL_EINVAL;
+  if (a->M == 0) return QL_OK;  // before the arrays: those without elements may be null
   if ((a->q != nullptr) != (a->q_out != nullptr) || (a->k != nullptr) != (a->k_out != nullptr) ||
       (a->v != nullptr) != (a->v_out != nullptr))
     return QL_EINVAL;
   if ((a->q && a->q_heads < 1) || ((a->k || a->v) && a->kv_heads < 1)) return QL_EINVAL;
   if ((!a->q && a->q_weight) || (!a->k && a->k_weight)) return QL_EINVAL;
-  if (a->M == 0) return QL_OK;
   if (!a->q && !a->k && !a->v) return QL_EINVAL;
   if (a->pairs > 0 && (!a->freqs || !a->positions || a->axes < 1)) return QL_EINVAL;
   const int64_t D = a->head_dim;

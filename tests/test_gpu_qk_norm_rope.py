@@ -262,3 +262,15 @@ def test_streams_device_and_graph(torch):
         for a, b in zip(outs, eager):
             assert torch.equal(a, b)
     assert outs[0].abs().sum() > 0
+
+
+def test_no_rows(torch):
+    """An empty batch is nothing to do, with weights, tables and tensors of their own or slices of longer ones."""
+    D = 64
+    weight, freqs = torch.ones(D, device="cuda"), torch.ones(D // 2, device="cuda")
+    full = torch.zeros((3, 8, D), dtype=torch.bfloat16, device="cuda")
+    for x in (full[:0], torch.empty((0, 8, D), dtype=torch.bfloat16, device="cuda")):
+        outs = [torch.empty((0, n, D), dtype=torch.bfloat16, device="cuda") for n in (4, 2, 2)]
+        ql.qlinear_qk_norm_rope(0, D, q=x[:, :4], k=x[:, 4:6], v=x[:, 6:], q_out=outs[0], k_out=outs[1], v_out=outs[2],
+                                norm=KIND["rms"], q_weight=weight, k_weight=weight, freqs=freqs,
+                                positions=torch.empty((3, 0), dtype=torch.int32, device="cuda"))

@@ -120,6 +120,15 @@ def test_qk_null_and_empty(lib):
     assert lib.qlinear_qk_norm_rope(ctypes.byref(_qk(M=0)), None) == ql.QL_OK
 
 
+@pytest.mark.parametrize("kw", [dict(q=0, k=0, v=0, q_out=0, k_out=0, v_out=0, positions=0), dict(q=0, k=0, v=0),
+                                dict(q=0, q_out=0), dict(k_out=0, v_out=0)])
+def test_qk_without_rows_has_null_arrays(lib, kw):
+    """Tensors without elements give null pointers, beside weights and outputs that are there."""
+    assert lib.qlinear_qk_norm_rope(ctypes.byref(_qk(M=0, **kw)), None) == ql.QL_OK
+    for bad, status in ((dict(head_dim=60), ql.QL_EUNSUPPORTED), (dict(norm=3), ql.QL_EINVAL), (dict(pairs=36), ql.QL_EINVAL)):
+        assert lib.qlinear_qk_norm_rope(ctypes.byref(_qk(M=0, **kw, **bad)), None) == status
+
+
 def _att(**kw):
     a = ql.ql_attention_args()
     base = dict(q=0x1000, k=0x2000, v=0x3000, out=0x4000, q_ld=512, k_ld=128, v_ld=128, out_ld=512, Mq=16, Mk=5000, q_heads=8,
