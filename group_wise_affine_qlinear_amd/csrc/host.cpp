@@ -1175,6 +1175,7 @@ QL_API int qlinear_attention(const ql_attention_args *a, void *stream) {
   if (!a->q || !a->out || (a->Mk > 0 && (!a->k || !a->v))) return QL_EINVAL;
   const int64_t q_row = a->q_heads * a->head_dim, kv_row = a->kv_heads * a->head_dim;
   if (a->q_ld < q_row || a->out_ld < q_row || (a->Mk > 0 && (a->k_ld < kv_row || a->v_ld < kv_row))) return QL_EINVAL;
+  if (a->out == a->q && a->out_ld != a->q_ld && a->Mq > 1) return QL_EINVAL;
   if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->out) || !aligned16(a->workspace) ||
       !on_elements(a->q_offsets, 4) || !on_elements(a->k_offsets, 4) || a->q_ld % 8 || a->out_ld % 8 ||
       (a->Mk > 0 && (a->k_ld % 8 || a->v_ld % 8)))

@@ -675,14 +675,15 @@ typedef struct ql_attention_args {
  * pieces and joined by a second launch; without one they are not, which is
  * slower for few queries. out may be q (of the same pitch) and overlaps no
  * input otherwise.
- * Returns QL_EINVAL for bad sizes, pitches, heads, scale or missing arrays,
- * QL_EALIGN for q, k, v, out or workspace not 16-byte aligned, pitches that
- * are not multiples of 8 or offsets not aligned to 4, QL_EUNSUPPORTED for a
- * head_dim that is not served or sizes above the limits, QL_EWORKSPACE for a
- * workspace that is too small. Mq == 0 is a no-op; with Mk == 0 every query of
- * a sample gets zeros (k, v and key_mask may be NULL). Calls that share one
- * workspace must not overlap in time; nothing in it is kept from one call to
- * the next. No allocation, no synchronization.
+ * Returns QL_EINVAL for bad sizes, pitches (out in place with another one
+ * included), heads, scale or missing arrays, QL_EALIGN for q, k, v, out or
+ * workspace not 16-byte aligned, pitches that are not multiples of 8 or
+ * offsets not aligned to 4, QL_EUNSUPPORTED for a head_dim that is not served
+ * or sizes above the limits, QL_EWORKSPACE for a workspace that is too small.
+ * Mq == 0 is a no-op; with Mk == 0 every query of a sample gets zeros (k, v
+ * and key_mask may be NULL). Calls that share one workspace must not overlap
+ * in time; nothing in it is kept from one call to the next. No allocation, no
+ * synchronization.
  */
 int qlinear_attention(const ql_attention_args *args, void *stream);
 

@@ -188,6 +188,15 @@ def test_attention_refusals(lib, kw, status):
     assert lib.qlinear_attention(ctypes.byref(_att(**kw)), None) == status
 
 
+def test_attention_in_place_has_one_pitch(lib):
+    """Rows of out that do not lie on those of q would be overwritten before other blocks read them."""
+    kw = dict(out=0x1000, out_ld=520, workspace_bytes=0)
+    assert lib.qlinear_attention(ctypes.byref(_att(**kw)), None) == ql.QL_EINVAL
+    # the same pitch, or one row, goes on to the next check
+    for more in (dict(out_ld=512), dict(Mq=1)):
+        assert lib.qlinear_attention(ctypes.byref(_att(**{**kw, **more})), None) == ql.QL_EWORKSPACE
+
+
 def test_attention_null_and_empty(lib):
     assert lib.qlinear_attention(None, None) == ql.QL_EINVAL
     assert lib.qlinear_attention(ctypes.byref(_att(Mq=0)), None) == ql.QL_OK
