@@ -981,7 +981,7 @@ def qlinear_attention(q, k, v, out, *, scale=None, q_offsets=None, k_offsets=Non
 def qlinear_rope_table_host(theta, pairs_per_axis, order=QL_ROPE_AXES_OWN):
     """C ``qlinear_rope_table_host``: (freqs fp32, axis int32) arrays for ``qlinear_qk_norm_rope``."""
     n = np.ascontiguousarray(pairs_per_axis, dtype=np.int64)
-    pairs = max(int(n.sum()), 0)
+    pairs = min(max(int(n.sum()), 0), 65536)  # more are refused before anything is written
     freqs, axis = np.empty(pairs, dtype=np.float32), np.empty(pairs, dtype=np.int32)
     _check(load_library().qlinear_rope_table_host(theta, n.size, n.ctypes.data, order, freqs.ctypes.data, axis.ctypes.data),
            "qlinear_rope_table_host")

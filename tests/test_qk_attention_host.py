@@ -58,6 +58,13 @@ def test_rope_table(order):
         ql.qlinear_rope_table_host(100.0, [])
 
 
+@pytest.mark.parametrize("pairs", [[65537], [1 << 45], [65536, 1], [1 << 62, 1 << 62], [1 << 45, -(1 << 45)], [4, -1]])
+def test_rope_table_refuses_sizes(pairs):
+    """More pairs than a table has are refused by the library, before memory is taken for them."""
+    with pytest.raises(ql.QLinearError):
+        ql.qlinear_rope_table_host(100.0, pairs)
+
+
 def _qk(**kw):
     a = ql.ql_qk_args()
     base = dict(M=4, head_dim=64, q_heads=4, kv_heads=2, q=0x1000, k=0x2000, v=0x3000, q_ld=256, k_ld=128, v_ld=128, in_dtype=0,
