@@ -669,8 +669,9 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
   auto chunk = [&](const unsigned char *kb, const unsigned char *vb, f32x16 (&x)[NQ], f32x16 (&y)[NQ], uint32_t valid, Copies c2)
       __attribute__((always_inline)) {
     uint32_t p[NQ][8];
-    float e0 = 0.f, e1 = 0.f;
-    // half n of the 16 NQ: the exponents and the first power of two weights, then the second and their sum
+    float e0 = 0.f, e1 = 0.f, sum = 0.f;
+    // half n of the 16 NQ: the exponents and the first power of two weights, then the second and their sum. A chunk's
+    // weights are added up by themselves before they meet the sum so far, which so takes no more additions than the outputs.
     auto half = [&](int n) __attribute__((always_inline)) {
       const int i = n / 16, r = n % 16 / 2 * 2;
       if (n % 2 == 0) {
@@ -679,8 +680,9 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
       } else {
         p[i][r / 2] = pack_bf16(e0, __builtin_amdgcn_exp2f(e1));
         const bf16x2 one = {(__bf16)1.f, (__bf16)1.f};
-        st.l[i] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p[i][r / 2]), one, st.l[i], false);
-        asm volatile("" : "+v"(p[i][r / 2]), "+v"(st.l[i]));
+        sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p[i][r / 2]), one, r == 0 ? 0.f : sum, false);
+        asm volatile("" : "+v"(p[i][r / 2]), "+v"(sum));
+        if (r == 14) st.l[i] += sum;
       }
     };
     bf16x8 kf[3];
@@ -857,8 +859,10 @@ __device__ __forceinline__ void weights(State<DP> &st, f32x16 s, float c, uint32
     const float b = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r + 1], c, -st.m[0]));
     w[r / 2] = pack_bf16(a, b);
   }
+  float sum = 0.f;  // of these keys alone first: the sum so far takes no more additions than the outputs
 #pragma unroll
-  for (int r = 0; r < 8; ++r) st.l[0] += bf16_lo(w[r]) + bf16_hi(w[r]);
+  for (int r = 0; r < 8; ++r) sum += bf16_lo(w[r]) + bf16_hi(w[r]);
+  st.l[0] += sum;
   p[0] = as_bf16x8(u32x4{w[0], w[1], w[2], w[3]});
   p[1] = as_bf16x8(u32x4{w[4], w[5], w[6], w[7]});
 }
@@ -1176,6 +1180,8 @@ AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, bool offse
   }
   p.whole = (int)(tiles - p.cut);
   p.blocks = (offsets ? tiles : p.whole) - p.rest + p.pieces;
+  p.longest = p.cut > 0 && p.whole == 0 && !offsets ? (int64_t)p.per * unit : Mk;
+  if (all) p.longest = (p.longest + 3) / 4;  // the waves of a block divide them
   p.partial_bytes = (size_t)p.pieces * p.rows * (dp + 2) * sizeof(float);
   return p;
 }

@@ -1039,6 +1039,9 @@ constexpr int64_t kMaxHeads = 65536;
 constexpr int64_t kMaxAttentionRows = int64_t(1) << 30;
 constexpr int64_t kMaxAttentionPitch = int64_t(1) << 22;  // 64 rows of it within a 31-bit offset
 constexpr int64_t kMaxSamples = int64_t(1) << 20;
+// Keys that a wave sums over: 2^18 additions of 16 keys each, which lose up to 2^-6 of a sum in fp32 if all are rounded
+// the same way (equal weights of equal values), and all of it 64 times later.
+constexpr int64_t kMaxSummedKeys = int64_t(1) << 22;
 
 bool head_dim_ok(int64_t D) { return D >= 8 && D <= kMaxHeadDim && D % 8 == 0; }
 
@@ -1185,6 +1188,7 @@ QL_API int qlinear_attention(const ql_attention_args *a, void *stream) {
     return QL_EUNSUPPORTED;
   const ql::AttentionPlan p = ql::attention_plan(a->Mq, a->Mk, samples, a->q_offsets != nullptr, (int)a->q_heads,
                                                  (int)a->kv_heads, (int)a->head_dim, a->workspace != nullptr);
+  if (!a->q_offsets && p.longest > kMaxSummedKeys) return QL_EUNSUPPORTED;
   if (a->workspace && a->workspace_bytes < p.partial_bytes) return QL_EWORKSPACE;
   ql::AttentionArgs k{};
   k.q = static_cast<const uint16_t *>(a->q);

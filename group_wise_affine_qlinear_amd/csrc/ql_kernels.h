@@ -248,6 +248,7 @@ struct AttentionPlan {
   int64_t rest;          // last tiles that go 32 rows to a block instead, from tile rest_from on
   int rest_from;
   int64_t blocks;        // tiles and pieces at most
+  int64_t longest;       // keys that one wave sums over, of a sample with all of them
   size_t partial_bytes;
 };
 AttentionPlan attention_plan(int64_t Mq, int64_t Mk, int64_t samples, bool offsets, int q_heads, int kv_heads, int D,

@@ -670,6 +670,12 @@ typedef struct ql_attention_args {
  * Scores, maxima, sums and outputs are fp32; the weights p enter the second
  * product as bf16 and their sum is that of the rounded weights; out is rounded
  * once. No atomics: results are reproducible bit for bit.
+ * A block adds up its keys 16 at a time in fp32, so over n keys of one sample
+ * that are not cut into pieces a sum may lose up to n * 2^-28 of the weighted
+ * mean of |v| (a quarter of that where a sample has up to 32 rows of a key head
+ * on average, q_heads / kv_heads rows a query): 2^-8, as much as the output's
+ * rounding, from 2^20 keys on. Without offsets, more than 2^22 such keys (2^24
+ * with few rows) are refused; a sample between offsets should not have more.
  * With a workspace the keys of tiles that would leave compute units idle
  * (single queries over many keys, the last tiles of a large call) are cut into
  * pieces and joined by a second launch; without one they are not, which is
@@ -678,8 +684,8 @@ typedef struct ql_attention_args {
  * Returns QL_EINVAL for bad sizes, pitches (out in place with another one
  * included), heads, scale or missing arrays, QL_EALIGN for q, k, v, out or
  * workspace not 16-byte aligned, pitches that are not multiples of 8 or
- * offsets not aligned to 4, QL_EUNSUPPORTED for a head_dim that is not served
- * or sizes above the limits, QL_EWORKSPACE for a workspace that is too small.
+ * offsets not aligned to 4, QL_EUNSUPPORTED for a head_dim that is not served,
+ * sizes above the limits or too many keys in one sum, QL_EWORKSPACE for a workspace that is too small.
  * Mq == 0 is a no-op; with Mk == 0 every query of a sample gets zeros (k, v
  * and key_mask may be NULL). Calls that share one workspace must not overlap
  * in time; nothing in it is kept from one call to the next. No allocation, no

@@ -210,6 +210,20 @@ def test_attention_null_and_empty(lib):
     assert lib.qlinear_attention(ctypes.byref(_att(samples=0)), None) == ql.QL_OK
 
 
+def test_attention_keys_of_one_sum(lib):
+    """Keys that nothing cuts are refused where fp32 sums lose too much, but for samples, whose lengths the host does not see."""
+    one = dict(samples=0, q_offsets=0, k_offsets=0)
+    # whole tiles of many rows; rows that four waves share; keys that are cut
+    for kw, most in ((dict(Mq=4608, q_heads=18, kv_heads=18, head_dim=256, q_ld=4608, k_ld=4608, v_ld=4608, out_ld=4608), 1 << 22),
+                     (dict(Mq=300000, q_heads=2, kv_heads=2), 1 << 22)):
+        assert lib.qlinear_attention(ctypes.byref(_att(Mk=most, **one, **kw)), None) == ql.QL_EWORKSPACE
+        assert lib.qlinear_attention(ctypes.byref(_att(Mk=most + 1, **one, **kw)), None) == ql.QL_EUNSUPPORTED
+        assert lib.qlinear_attention(ctypes.byref(_att(Mk=most + 1, **{**one, **kw, "workspace": 0})), None) == ql.QL_EUNSUPPORTED
+        assert lib.qlinear_attention(ctypes.byref(_att(Mk=1 << 30, **kw)), None) == ql.QL_EWORKSPACE
+    assert lib.qlinear_attention(ctypes.byref(_att(Mk=(1 << 24) + 1, Mq=4, workspace=0, **one)), None) == ql.QL_EUNSUPPORTED
+    assert lib.qlinear_attention(ctypes.byref(_att(Mk=1 << 30, Mq=4, **one)), None) == ql.QL_EWORKSPACE
+
+
 def test_attention_workspace(lib):
     for case in ((16, 5000, 3, 8, 2, 64), (1, 65536, 1, 18, 18, 256), (77, 16896, 1, 24, 24, 128), (4608, 4608, 1, 18, 18, 256)):
         need = ql.qlinear_attention_workspace_bytes(*case)
