@@ -416,8 +416,11 @@ __device__ __forceinline__ uint16_t *out_row(const AttentionArgs &a, const Work 
   return a.out + (int64_t)(w.s.q0 + m) * a.out_ld + (int64_t)(w.head * a.group + r - m * a.group) * a.D;
 }
 
-// Sum over both halves, 1 / it, or 0 where there is no weight at all.
-__device__ __forceinline__ float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
+// 1 / the sum of a query's weights; 0 for a query without a score (its maximum is still the lowest). Scores from some
+// 2^31 on, whose maximum is rounded to multiples of 2^8, can have all weights vanish: that is no zero, but NaN.
+__device__ __forceinline__ float reciprocal(float l, float m) {
+  return l != 0.f ? 1.f / l : m == kLowest ? 0.f : __builtin_nanf("");
+}
 
 // ------------------------------------------------------------------ tiles of many rows
 
@@ -798,7 +801,7 @@ __global__ __launch_bounds__(256, 1) void attention_kernel(AttentionArgs a) {
   unsigned char *const rows = wave == 0 ? k0 : wave == 1 ? k1 : wave == 2 ? v0 : v1;
   constants<NQ>([&](auto block) __attribute__((always_inline)) {
     constexpr int i = decltype(block)::value;
-    const float f = reciprocal(st.l[i] + other_half(st.l[i]));
+    const float f = reciprocal(st.l[i] + other_half(st.l[i]), st.m[i]);
     const int q = 32 * i + (lane & 31);
     constants<4 * kTiles>([&](auto four) __attribute__((always_inline)) {
       constexpr int j = decltype(four)::value / 4, g = decltype(four)::value % 4;
@@ -1000,7 +1003,7 @@ __global__ __launch_bounds__(256, 1) void attention_few_kernel(AttentionArgs a) 
         part[BQ * (DP + 1) + rt] = sum;
       }
     } else if (d4 * 4 < a.D) {
-      const float inv = reciprocal(sum);
+      const float inv = reciprocal(sum, m);
       *reinterpret_cast<u32x2 *>(out_row(a, w, w.tile * BQ + rt) + d4 * 4) =
           u32x2{pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv)};
     }
@@ -1064,7 +1067,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a) {
           for (int e = 0; e < 4; ++e) v[j][e] = __builtin_fmaf(x[g][j][e], f, v[j][e]);
       }
     }
-    const float inv = reciprocal(sum);
+    const float inv = reciprocal(sum, m);
     uint16_t *o = out_row(a, w, w.tile * BQ + rt) + d4 * 4;
 #pragma unroll
     for (int j = 0; j < N; ++j)

@@ -664,7 +664,9 @@ typedef struct ql_attention_args {
  * first offset, or padding from the last on) are left as they are. What hidden keys and their values, other
  * samples' rows and rows outside the samples hold, infinities and NaN
  * included, never reaches an output; in a query's own values they give an
- * infinity or NaN. Offsets and mask are read on the device, so a captured
+ * infinity or NaN. Scores scale * q . k up to 2^28 in magnitude are served, and
+ * values v of which n keys' |v| add up to at most 2^100; a query with larger
+ * ones may give an infinity or NaN, but no zeros. Offsets and mask are read on the device, so a captured
  * graph serves other lengths after they are overwritten. Offsets that
  * decrease give unspecified results, but no access outside the arrays.
  * Scores, maxima, sums and outputs are fp32; the weights p enter the second

@@ -191,6 +191,45 @@ def test_values_that_are_not_finite_stay_with_their_query(torch, nq, nk, hq, D, 
     assert torch.equal(out, clean)
 
 
+@pytest.mark.parametrize("nq,nk,D,path", [(3, 500, 64, "rows32_slots0"), (3, 4000, 256, "rows32_slots512"),
+                                          (100, 500, 128, "rows128_slots0"), (100, 1500, 192, "rows128_slots256"),
+                                          (2000, 9000, 256, "rows256_slots256"), (33024, 4100, 64, "rows256_slots512")])
+def test_large_scores_and_values(torch, nq, nk, D, path):
+    """One key is far ahead of the others, so its values are what every query gives, bit for bit: the other weights vanish,
+    and a bf16 value times a bf16 weight is exact in fp32 and so divided by the weight again. With scores beyond those
+    that are served a query may be NaN, but is never zeros."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    base = torch.randn((1, 1, D), generator=g, device="cuda").to(torch.bfloat16)
+    q = base.repeat(nq, 1, 1)
+    k = (0.2 * torch.randn((nk, 1, D), generator=g, device="cuda")).to(torch.bfloat16)
+    best = nk * 2 // 3
+    k[best] = base[0]
+    v = torch.randn((nk, 1, D), generator=g, device="cuda").to(torch.bfloat16)
+    square = (base.double() ** 2).sum().item()
+    out = torch.empty_like(q)
+    for sign in (1.0, -1.0):
+        # all scores far below zero: the best key's, at -2^lg, is the least of them
+        if sign < 0:
+            k = (base * 4).expand(nk, 1, D).contiguous()
+            k[best] = base[0]
+            q = -q
+        for lg in (10, 20, 25.5, 26, 28, 30, 31, 32, 33, 34, 50):
+            ql.qlinear_attention(q, k, v, out, scale=0.97 * 2.0 ** lg / square)
+            assert ql.qlinear_last_path() == "attention_" + path
+            right = (out == v[best]).all(dim=2)
+            served = lg <= (28 if sign > 0 else 26)  # the other keys' scores are four times as far below
+            assert right.all() if served else (right | ~torch.isfinite(out).all(dim=2)).all(), lg
+    out.fill_(7.0)
+    ql.qlinear_attention(q, k, v, out, key_mask=torch.zeros(nk, dtype=torch.bool, device="cuda"), scale=1e9)
+    assert (out == 0).all()
+    v = (v.abs() + 1) * 2.0 ** 80  # 9000 of them below 2^100
+    ql.qlinear_attention(q, k, v, out, scale=0.97 * 2.0 ** 26 / square)
+    assert (out == v[best]).all()
+    ql.qlinear_attention(q, k, v, out, scale=1e-30)
+    mean = v.double().mean(dim=0)
+    assert ((out.double() - mean).abs() <= 2.0 ** -7 * mean).all()  # the weights' rounding and the output's, 2^-8 each
+
+
 @pytest.mark.parametrize("nq,nk,hq,hkv,D,path", [(8237, 1100, 8, 2, 88, "rows128_slots512"), (8300, 2200, 8, 8, 256, "rows256_slots256"),
                                                  (8300, 700, 8, 8, 256, "rows256_slots0_rest32"),
                                                  (32850, 4100, 4, 1, 64, "rows256_slots512")])
