@@ -210,6 +210,20 @@ def test_attention_null_and_empty(lib):
     assert lib.qlinear_attention(ctypes.byref(_att(samples=0)), None) == ql.QL_OK
 
 
+@pytest.mark.parametrize("Mq,samples,group,heads,tile", [
+    (1 << 20, 1 << 20, 1, 15, 32), (1 << 20, 1 << 20, 1, 16, 32), (1 << 20, 1 << 18, 8, 32, 32), (1 << 20, 1 << 18, 8, 31, 32),
+    (1 << 27, 1, 8, 8, 128), (1 << 23, 1, 8, 64, 128), (1 << 27, 100, 1, 15, 128), (1 << 27, 100, 1, 16, 128),
+    (1 << 30, 1 << 20, 1, 1, 128), (1 << 30, 1 << 20, 1, 2, 128)])
+def test_attention_limit_of_tiles(lib, Mq, samples, group, heads, tile):
+    """What the header says is served and what is refused; an address that is not aligned is looked at behind the sizes."""
+    kw = dict(Mq=Mq, samples=samples, q_heads=group * heads, kv_heads=heads, head_dim=128, q=0x1008, q_ld=group * heads * 128,
+              out_ld=group * heads * 128, k_ld=heads * 128, v_ld=heads * 128)
+    tiles = (-(-Mq * group // tile) + samples) * heads
+    assert tiles < 2 ** 24 - 2048 or tiles >= 2 ** 24
+    status = ql.QL_EALIGN if tiles < 2 ** 24 else ql.QL_EUNSUPPORTED
+    assert lib.qlinear_attention(ctypes.byref(_att(**kw)), None) == status
+
+
 def test_attention_keys_of_one_sum(lib):
     """Keys that nothing cuts are refused where fp32 sums lose too much, but for samples, whose lengths the host does not see."""
     one = dict(samples=0, q_offsets=0, k_offsets=0)
