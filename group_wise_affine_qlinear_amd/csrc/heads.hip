@@ -29,10 +29,6 @@ namespace {
 
 // Sum (or maximum of magnitudes) over the aligned groups of 2^lg lanes, in a
 // fixed order, in every lane of the group.
-template <int CTRL, typename Op>
-__device__ __forceinline__ float dpp(float v, Op op) {
-  return op(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false)));
-}
 template <typename Op>
 __device__ __forceinline__ float group_all(float v, int lg, Op op) {
   v = dpp<0xB1>(v, op);                // quad_perm [1, 0, 3, 2]
@@ -46,13 +42,6 @@ __device__ __forceinline__ float group_all(float v, int lg, Op op) {
   }
   return v;
 }
-
-struct Sum {
-  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
-struct Max {
-  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
 
 // The 8 values of a lane: four at `lo` and four at `hi` of its head.
 template <typename T, bool VEC>

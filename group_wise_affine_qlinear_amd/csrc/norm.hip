@@ -29,14 +29,7 @@ namespace {
 struct None {};
 
 // op over the 64 lanes by DPP moves in a fixed order (pairs, quads, half rows
-// and rows of 16, then rows 0-1 and 2-3, then both halves), in every lane. A
-// lane that a move leaves out takes `op(v, 0)`: the sum, and the maximum of
-// magnitudes.
-template <int CTRL, int ROWS, typename Op>
-__device__ __forceinline__ float dpp(float v, Op op) {
-  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, false);
-  return op(v, __builtin_bit_cast(float, o));
-}
+// and rows of 16, then rows 0-1 and 2-3, then both halves), in every lane.
 template <typename Op>
 __device__ __forceinline__ float row16_all(float v, Op op) {
   v = dpp<0xB1, 0xF>(v, op);   // quad_perm [1, 0, 3, 2]
@@ -51,13 +44,6 @@ __device__ __forceinline__ float wave_all(float v, Op op) {
   v = dpp<0x143, 0xC>(v, op);  // row_bcast:31 into rows 2 and 3
   return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
 }
-
-struct Sum {
-  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
-struct Max {  // of magnitudes
-  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
 
 // The place of a lane in its row, and the LDS lines of the row's reductions.
 struct Place {

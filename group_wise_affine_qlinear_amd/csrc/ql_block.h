@@ -1,5 +1,6 @@
 // Device helpers shared by the operators around a projection (norm.hip,
-// adapters.hip): fp32 / bf16 element access and rounding.
+// adapters.hip) and between two (heads.hip, attention.hip): fp32 / bf16 element
+// access and rounding, reductions over lanes.
 #pragma once
 
 #include "ql_device.h"
@@ -28,6 +29,20 @@ struct BF16 {
   static __device__ __forceinline__ void store(void *p, int64_t i, float v) {
     static_cast<uint16_t *>(p)[i] = bf16_bits(v);
   }
+};
+
+// op over a lane and the one that a DPP move gives it. A lane that the move
+// leaves out takes `op(v, 0)`: the sum, and the maximum of magnitudes.
+template <int CTRL, int ROWS = 0xF, typename Op>
+__device__ __forceinline__ float dpp(float v, Op op) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, false);
+  return op(v, __builtin_bit_cast(float, o));
+}
+struct Sum {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct Max {  // of magnitudes
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
 
 }  // namespace ql
