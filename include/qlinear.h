@@ -620,7 +620,8 @@ typedef struct ql_qk_args {
  * Returns QL_EINVAL for bad sizes, pitches, types, norms, eps or missing
  * arrays, QL_EALIGN for a pointer not aligned to its element, QL_EUNSUPPORTED
  * for a head_dim or number of pairs that is not served or sizes above the
- * limits. M == 0 is a no-op. No scratch, no allocation, no synchronization.
+ * limits. M == 0 is a no-op (the arrays may be NULL). No scratch, no
+ * allocation, no synchronization.
  */
 int qlinear_qk_norm_rope(const ql_qk_args *args, void *stream);
 
@@ -661,13 +662,14 @@ typedef struct ql_attention_args {
  * Ideogram 4 paper notes, section 2.4) or another sequence of another length
  * (an encoder's states). A query without a kept key, or whose scores are all
  * minus infinity, gives zeros. Queries that belong to no sample (before the
- * first offset, or padding from the last on) are left as they are. What hidden keys and their values, other
- * samples' rows and rows outside the samples hold, infinities and NaN
- * included, never reaches an output; in a query's own values they give an
- * infinity or NaN. Scores scale * q . k up to 2^28 in magnitude are served, and
- * values v of which n keys' |v| add up to at most 2^100; a query with larger
- * ones may give an infinity or NaN, but no zeros. Offsets and mask are read on the device, so a captured
- * graph serves other lengths after they are overwritten. Offsets that
+ * first offset, or padding from the last on) are left as they are. What hidden
+ * keys and their values, other samples' rows and rows outside the samples hold,
+ * infinities and NaN included, never reaches an output; in a query's own values
+ * they give an infinity or NaN. Scores scale * q . k up to 2^28 in magnitude
+ * are served, and values v of which n keys' |v| add up to at most 2^100; a
+ * query with larger ones may give an infinity or NaN, and zeros only if all its
+ * scores lie below fp32's range. Offsets and mask are read on the device, so a
+ * captured graph serves other lengths after they are overwritten. Offsets that
  * decrease give unspecified results, but no access outside the arrays.
  * Scores, maxima, sums and outputs are fp32; the weights p enter the second
  * product as bf16 and their sum is that of the rounded weights; out is rounded
@@ -693,11 +695,11 @@ typedef struct ql_attention_args {
  * included), heads, scale or missing arrays, QL_EALIGN for q, k, v, out or
  * workspace not 16-byte aligned, pitches that are not multiples of 8 or
  * offsets not aligned to 4, QL_EUNSUPPORTED for a head_dim that is not served,
- * sizes above the limits or too many keys in one sum, QL_EWORKSPACE for a workspace that is too small.
- * Mq == 0 is a no-op; with Mk == 0 every query of a sample gets zeros (k, v
- * and key_mask may be NULL). Calls that share one workspace must not overlap
- * in time; nothing in it is kept from one call to the next. No allocation, no
- * synchronization.
+ * sizes above the limits or too many keys in one sum, QL_EWORKSPACE for a
+ * workspace that is too small. Mq == 0 is a no-op; with Mk == 0 every query of
+ * a sample gets zeros (k, v and key_mask may be NULL). Calls that share one
+ * workspace must not overlap in time; nothing in it is kept from one call to
+ * the next. No allocation, no synchronization.
  */
 int qlinear_attention(const ql_attention_args *args, void *stream);
 
