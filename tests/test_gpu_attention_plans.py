@@ -242,6 +242,21 @@ def test_in_place(torch, nq, nk, hq, hkv, D, path):
     assert torch.equal(again, want)
 
 
+@pytest.mark.parametrize("nq,nk,D", [(20, 700, 64), (300, 600, 128), (300, 8100, 256)])
+@pytest.mark.parametrize("far", ["q", "k", "v", "out"])
+def test_largest_pitches(torch, nq, nk, D, far):
+    """One of the arrays with the longest rows that are served: byte offsets pass 31 bits within queries and 32 within keys,
+    29 within 64 rows."""
+    q, k, v = make(torch, nq, nk, 2, 2, D, 19)
+    want = check(torch, q, k, v)
+    t = {"q": q, "k": k, "v": v, "out": torch.empty_like(q)}
+    long = torch.full((t[far].shape[0], 1 << 22), 7.0, dtype=torch.bfloat16, device="cuda")
+    t[far] = long[:, 8:8 + 2 * D].unflatten(1, (2, D)).copy_(t[far])
+    ql.qlinear_attention(t["q"], t["k"], t["v"], t["out"])
+    assert torch.equal(t["out"], want)
+    assert (long[:, :8] == 7.0).all() and (long[:, 8 + 2 * D:] == 7.0).all()
+
+
 # queries, keys, samples, query heads, key heads, D
 DEVICE = [(40, 20000, 4, 2, 2, 64), (700, 20000, 4, 2, 2, 128), (900, 20000, 4, 2, 2, 256), (3000, 9000, 4, 2, 1, 192)]
 

@@ -274,3 +274,35 @@ def test_no_rows(torch):
         ql.qlinear_qk_norm_rope(0, D, q=x[:, :4], k=x[:, 4:6], v=x[:, 6:], q_out=outs[0], k_out=outs[1], v_out=outs[2],
                                 norm=KIND["rms"], q_weight=weight, k_weight=weight, freqs=freqs,
                                 positions=torch.empty((3, 0), dtype=torch.int32, device="cuda"))
+
+
+def test_most_rows(torch):
+    """2^24 - 1 rows of one small head: the largest grid. Values are turned by whole and half turns, which change at most
+    the sign; the angle of pi is off by less than 2^-22, the sine with it, and the values are at most 3."""
+    M, D = (1 << 24) - 1, 8
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q = torch.randint(-3, 4, (M, 1, D), generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.empty_like(q)
+    positions = torch.arange(M, device="cuda", dtype=torch.int32) % 4
+    freqs = torch.full((D // 2,), np.pi, dtype=torch.float32, device="cuda")
+    ql.qlinear_qk_norm_rope(M, D, q=q, q_out=out, freqs=freqs, positions=positions)
+    want = torch.where((positions % 2 == 1)[:, None, None], -q, q).float()
+    assert ((out.float() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -18).all()
+
+
+def test_rows_past_4_gib(torch):
+    """Rows whose byte offsets pass 32 bits, in inputs and outputs, give what the same rows give side by side."""
+    M, D, pitch = 2100, 64, 1 << 20  # 4.4 GB each
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn((M, 4, D), generator=g, device="cuda").to(torch.bfloat16)
+    far, far_out = (torch.zeros((M, pitch), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    far[:, 3 * D:7 * D].copy_(x.view(M, 4 * D))
+    freqs = torch.rand(D // 2, generator=g, device="cuda")
+    kw = dict(norm=KIND["rms"], freqs=freqs, positions=torch.arange(M, device="cuda", dtype=torch.int32))
+    part = lambda t, n: t[:, n * D:(n + 1) * D].unflatten(1, (1, D))  # noqa: E731
+    outs = [torch.empty((M, 1, D), dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    ql.qlinear_qk_norm_rope(M, D, q=x[:, :1], k=x[:, 1:2], v=x[:, 2:3], q_out=outs[0], k_out=outs[1], v_out=outs[2], **kw)
+    ql.qlinear_qk_norm_rope(M, D, q=part(far, 3), k=part(far, 4), v=part(far, 5), q_out=part(far_out, 0),
+                            k_out=part(far_out, 1), v_out=part(far_out, 2), **kw)
+    assert torch.equal(far_out[:, :3 * D], torch.cat(outs, dim=1).view(M, 3 * D))
+    assert not far_out[:, 3 * D:].any()
